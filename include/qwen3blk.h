@@ -109,13 +109,46 @@ typedef struct {
   int s_max;
 } qwen3_kv_layer;
 
+/* One layer's KV cache in pages: k and v are [n_pages][Hkv][page_size][D], with page_size 16,
+ * 32, 64, 128 or 256 tokens and n_pages * Hkv * page_size below 2^31 - 256. fp8 = 0: bf16 (the
+ * scales are not read). fp8 = 1: e4m3 bytes with one fp32 scale per KV head, k_scale [Hkv]
+ * and v_scale [Hkv] (device, positive and finite): a byte stands for its e4m3 value times
+ * the head's scale, and a value x is stored as e4m3(x * (1 / scale)), rounded to nearest
+ * even, magnitudes above 448 saturated, NaN kept. The attention folds k_scale into the
+ * softmax factor and v_scale into the output. */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int n_pages;
+  int page_size;
+  int fp8;
+} qwen3_kv_pages;
+
+/* A ragged batch over a paged cache (host struct, device lists of int32). The new tokens of
+ * sequence b are rows q_start[b] .. q_start[b+1]-1 of the calls' token buffers, at positions
+ * ctx_len[b], ctx_len[b] + 1, ...; a sequence may have none. Position p of sequence b lives in
+ * page page_table[b * max_pages + p / page_size], slot p % page_size. Entries behind a
+ * sequence's last position are not read; sequences may share pages that no call writes.
+ * q_start must not decrease; rows q_start[B] .. n_tokens-1 belong to no sequence: they are not
+ * read as tokens and their outputs are left as they were. */
+typedef struct {
+  const int* q_start;    /* [B+1] */
+  const int* ctx_len;    /* [B] cached positions before this call's tokens */
+  const int* page_table; /* [B][max_pages] */
+  int B;
+  int max_pages;         /* max_pages * page_size below 2^31 - 256 */
+} qwen3_paged_batch;
+
 typedef enum {
   QWEN3_OP_BLOCK_PREFILL = 1,
   QWEN3_OP_BLOCK_DECODE = 2,
   QWEN3_OP_MOE_BLOCK = 3,
   QWEN3_OP_STACK_PREFILL = 4,
   QWEN3_OP_STACK_DECODE = 5,
-  QWEN3_OP_GENERATE = 6  /* qwen3_generate_greedy: T = prompt length */
+  QWEN3_OP_GENERATE = 6, /* qwen3_generate_greedy: T = prompt length */
+  QWEN3_OP_ATTENTION_PAGED = 7 /* qwen3_op_attention_paged: T = max_q (s_max: any positive value) */
 } qwen3_op;
 
 typedef enum { QWEN3_MODE_PREFILL = 0, QWEN3_MODE_DECODE = 1 } qwen3_mode;
@@ -354,6 +387,47 @@ int qwen3_op_attention_decode(const qwen3_config* cfg, const qwen3_bf16* qkv, lo
 int qwen3_op_attention_decode_noalloc(const qwen3_config* cfg, const qwen3_bf16* qkv, long long ldqkv, int B,
                                       const int* cache_len, const qwen3_kv_layer* kv, qwen3_bf16* o, long long ldo,
                                       void* stream);
+
+/* Per-head QK RMSNorm + rotate-half RoPE + paged KV-cache write of a ragged batch: the paged
+ * form of qwen3_op_qk_norm_rope. qkv [n_tokens, (Hq+2Hkv)*D] (row stride ldqkv): q heads are
+ * normalised, rotated and written to q_out [n_tokens, Hq*D] (stride ldq; q_out == qkv with
+ * ldq == ldqkv runs in place); k heads (normalised, rotated) and v heads are written to
+ * their pages. A token whose position is past max_pos or the page table is reported by the
+ * device as QWEN3_ECAPACITY, a negative position, a page id outside [0, n_pages) or a
+ * decreasing q_start as QWEN3_EINVAL; nothing of that token is written. */
+int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, long long ldqkv, int n_tokens,
+                                const qwen3_paged_batch* batch, const qwen3_bf16* q_norm, const qwen3_bf16* k_norm,
+                                const qwen3_kv_pages* kv, const float* rope, qwen3_bf16* q_out, long long ldq,
+                                void* stream);
+
+/* Causal GQA attention of a ragged batch's new tokens over the paged cache, which already
+ * holds them (qwen3_op_qk_norm_rope_paged): token t of sequence b attends to positions
+ * 0 .. ctx_len[b] + t. q [n_tokens, Hq*D] (post-norm, post-RoPE, stride ldq); o the same shape
+ * (stride ldo), bf16 (fp16 when cfg->gemm_f16). One call takes any mix of decode tokens
+ * (one new token) and prompt chunks.
+ *   max_q   upper bound (host) on the new tokens of any sequence; max_q == 1 selects the
+ *           decode form of the kernel
+ *   ws      qwen3_workspace_size(cfg, QWEN3_OP_ATTENTION_PAGED, B, max_q, any) bytes; calls that may
+ *           overlap on the GPU need workspaces of their own
+ * The device reports a sequence with a negative length or context, more than max_q tokens or
+ * tokens past row n_tokens as QWEN3_EINVAL and one past its page table as QWEN3_ECAPACITY, and
+ * leaves its rows of o as they were; a page id outside [0, n_pages) is reported as
+ * QWEN3_EINVAL, and that sequence's rows of o then hold no meaningful values. Cache rows behind
+ * a token's position are never used, whatever they hold (NaN included). */
+int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long long ldq, int n_tokens, int max_q,
+                             const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, qwen3_bf16* o, long long ldo,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Copies the batch's positions (ctx_len[b] .. ctx_len[b] + q_start[b+1] - q_start[b] - 1 of sequence b,
+ * all KV heads, k and v) from a contiguous cache [B][Hkv][s_max][D] into pages, quantising for
+ * e4m3 pages, or from pages into a contiguous cache, as bf16. n_tokens >= q_start[B] bounds the
+ * positions moved; everything else is left as it was. Moves a prompt that qwen3_block_prefill or
+ * qwen3_stack_forward cached into pages, and back for qwen3_block_decode. Errors as
+ * qwen3_op_qk_norm_rope_paged (a position past s_max: QWEN3_ECAPACITY). */
+int qwen3_op_kv_to_pages(const qwen3_config* cfg, const qwen3_kv_layer* src, int n_tokens,
+                         const qwen3_paged_batch* batch, const qwen3_kv_pages* dst, void* stream);
+int qwen3_op_kv_from_pages(const qwen3_config* cfg, const qwen3_kv_pages* src, int n_tokens,
+                           const qwen3_paged_batch* batch, const qwen3_kv_layer* dst, void* stream);
 
 /* out[r * ld_out] = argmax_j x[r * ldx + j], j < V (fp32 logits; ties: lower index; NaN
  * never chosen). V % 4 == 0, x and ldx 16-byte aligned in bytes. */

@@ -21,6 +21,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, ESHAPE, EALIGN, ECAPACITY, EWORKSPACE, ECUDA, ETIMEOUT, EDEVICE = 0, -1, -2, -3, -4, -5, -6, -7, -8
 OP_BLOCK_PREFILL, OP_BLOCK_DECODE, OP_MOE_BLOCK, OP_STACK_PREFILL, OP_STACK_DECODE, OP_GENERATE = 1, 2, 3, 4, 5, 6
+OP_ATTENTION_PAGED = 7
 MODE_PREFILL, MODE_DECODE = 0, 1
 EPI_STORE, EPI_RESID, EPI_SWIGLU = 0, 1, 2
 
@@ -40,6 +41,17 @@ class LayerWeights(ctypes.Structure):
 
 class KVLayer(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("s_max", ctypes.c_int)]
+
+
+class KVPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("fp8", ctypes.c_int)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 _vp, _i, _ll, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
@@ -76,6 +88,12 @@ _SIGS = {
     "qwen3_op_attention_prefill": ([_P(Config), _vp, _ll, _i, _i, _vp, _P(KVLayer), _vp, _ll, _vp], _i),
     "qwen3_op_attention_decode": ([_P(Config), _vp, _ll, _i, _vp, _P(KVLayer), _vp, _ll, _vp, _sz, _vp], _i),
     "qwen3_op_attention_decode_noalloc": ([_P(Config), _vp, _ll, _i, _vp, _P(KVLayer), _vp, _ll, _vp], _i),
+    "qwen3_op_qk_norm_rope_paged": ([_P(Config), _vp, _ll, _i, _P(PagedBatch), _vp, _vp, _P(KVPages), _vp, _vp, _ll,
+                                     _vp], _i),
+    "qwen3_op_attention_paged": ([_P(Config), _vp, _ll, _i, _i, _P(PagedBatch), _P(KVPages), _vp, _ll, _vp, _sz, _vp],
+                                 _i),
+    "qwen3_op_kv_to_pages": ([_P(Config), _P(KVLayer), _i, _P(PagedBatch), _P(KVPages), _vp], _i),
+    "qwen3_op_kv_from_pages": ([_P(Config), _P(KVPages), _i, _P(PagedBatch), _P(KVLayer), _vp], _i),
     "qwen3_op_embed": ([_vp, _i, _vp, _i, _i, _vp, _i, _i, _vp], _i),
     "qwen3_convert_to_f16": ([_vp, _vp, _sz, _vp], _i),
     "qwen3_op_argmax": ([_vp, _ll, _i, _i, _vp, _ll, _vp], _i),
@@ -200,6 +218,36 @@ def kv_layer(k, v, s_max: int) -> KVLayer:
     return KVLayer(_ptr(k), _ptr(v), s_max)
 
 
+def kv_pages(k, v, k_scale=None, v_scale=None) -> KVPages:
+    """Pages of one layer's cache: k and v [n_pages, Hkv, page_size, 128], bf16, or
+    float8_e4m3fn with fp32 scales [Hkv]. The struct holds raw pointers: keep the tensors."""
+    import torch
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[3] != 128:
+        raise ValueError("kv_pages: k and v must share their type and shape [n_pages, Hkv, page_size, 128]")
+    if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("kv_pages: pages are bfloat16 or float8_e4m3fn")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("kv_pages: pages must be contiguous")
+    fp8 = k.dtype == torch.float8_e4m3fn
+    if fp8:
+        for t in (k_scale, v_scale):
+            if t is None or t.dtype != torch.float32 or t.numel() != k.shape[1] or not t.is_contiguous():
+                raise ValueError("kv_pages: e4m3 pages need contiguous float32 k_scale and v_scale of one value per KV head")
+    return KVPages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[2], 1 if fp8 else 0)
+
+
+def paged_batch(q_start, ctx_len, page_table) -> PagedBatch:
+    """A ragged batch: int32 q_start [B+1], ctx_len [B], page_table [B, max_pages] (contiguous;
+    keep the tensors)."""
+    import torch
+    B = ctx_len.numel()
+    if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (q_start, ctx_len, page_table)):
+        raise ValueError("paged_batch: the lists must be contiguous int32 tensors")
+    if q_start.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("paged_batch: q_start has B + 1 entries and page_table is [B, max_pages]")
+    return PagedBatch(_ptr(q_start), _ptr(ctx_len), _ptr(page_table), B, page_table.shape[1])
+
+
 # ------------------------------------------------------------------------- block calls
 def block_prefill(cfg, w, x, B, T, start_pos, kv, rope, ws, stream=None) -> None:
     _check(lib.qwen3_block_prefill(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), B, T, _ptr(start_pos),
@@ -305,6 +353,37 @@ def op_attention_decode_noalloc(cfg, qkv, B, cache_len, kv, o, ldqkv=None, ldo=N
     _check(lib.qwen3_op_attention_decode_noalloc(ctypes.byref(cfg), _ptr(qkv), ld, B, _ptr(cache_len),
                                                  ctypes.byref(kv), _ptr(o), ldo or cfg.n_q_heads * cfg.head_dim,
                                                  _stream(stream)), "op_attention_decode_noalloc")
+
+
+def op_qk_norm_rope_paged(cfg, qkv, n_tokens, batch, q_norm, k_norm, pages, rope, q_out, ldqkv=None, ldq=None,
+                          stream=None) -> None:
+    """QK norm, rotation and paged cache write; q_out may be qkv (in place, ldq = ldqkv)."""
+    width = cfg.n_q_heads * cfg.head_dim
+    ld = ldqkv or width + 2 * cfg.n_kv_heads * cfg.head_dim
+    if ldq is None:
+        ldq = ld if q_out is qkv else width
+    _check(lib.qwen3_op_qk_norm_rope_paged(ctypes.byref(cfg), _ptr(qkv), ld, n_tokens, ctypes.byref(batch),
+                                           _ptr(q_norm), _ptr(k_norm), ctypes.byref(pages), _ptr(rope), _ptr(q_out),
+                                           ldq, _stream(stream)), "op_qk_norm_rope_paged")
+
+
+def op_attention_paged(cfg, q, n_tokens, max_q, batch, pages, o, ws, ldq=None, ldo=None, stream=None) -> None:
+    width = cfg.n_q_heads * cfg.head_dim
+    _check(lib.qwen3_op_attention_paged(ctypes.byref(cfg), _ptr(q), ldq or width, n_tokens, max_q,
+                                        ctypes.byref(batch), ctypes.byref(pages), _ptr(o), ldo or width, _ptr(ws),
+                                        ws.numel() * ws.element_size(), _stream(stream)), "op_attention_paged")
+
+
+def op_kv_to_pages(cfg, kv, n_tokens, batch, pages, stream=None) -> None:
+    """Contiguous cache (kv_layer) -> pages, the batch's positions."""
+    _check(lib.qwen3_op_kv_to_pages(ctypes.byref(cfg), ctypes.byref(kv), n_tokens, ctypes.byref(batch),
+                                    ctypes.byref(pages), _stream(stream)), "op_kv_to_pages")
+
+
+def op_kv_from_pages(cfg, pages, n_tokens, batch, kv, stream=None) -> None:
+    """Pages -> contiguous cache (kv_layer), the batch's positions."""
+    _check(lib.qwen3_op_kv_from_pages(ctypes.byref(cfg), ctypes.byref(pages), n_tokens, ctypes.byref(batch),
+                                      ctypes.byref(kv), _stream(stream)), "op_kv_from_pages")
 
 
 def op_embed(ids, n, embed, vocab, H, out, stream=None) -> None:

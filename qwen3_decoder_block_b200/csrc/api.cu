@@ -17,6 +17,7 @@
 #include "../../include/qwen3blk.h"
 #include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace q3 {
 
@@ -52,6 +53,16 @@ int launch_moe_permute(const int* idx, int T, int k, int E, const int* counts, i
                        int* perm_slot, int* inv_pos, const uint16_t* h, int H, uint16_t* a_perm, cudaStream_t s);
 int launch_moe_combine(const float* x1, const uint16_t* Y, const float* w, const int* inv_pos, int T, int k, int H,
                        void* out, bool out_f32, cudaStream_t s);
+
+int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens, const PagedBatch& pb,
+                              const KvPages& kv, int Hq, const uint16_t* qw, const uint16_t* kw, const float* rope,
+                              int max_pos, float eps, uint16_t* q_out, long long ldq, int* err, cudaStream_t s);
+int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_tokens, const PagedBatch& pb,
+                   const KvPages& kv, int* err, cudaStream_t s);
+int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int max_q, const PagedBatch& pb,
+                           const KvPages& kv, int Hq, void* scratch, uint16_t* out, long long ldo, int* err,
+                           cudaStream_t s, bool o_f16);
+size_t paged_attention_bytes(int B, int Hq, int Hkv, int max_q);
 
 // ----------------------------------------------------------------------------- errors
 static thread_local std::string g_last_error;
@@ -794,6 +805,52 @@ static int check_kv(const qwen3_config& c, const qwen3_kv_layer* kv, int T) {
   return 0;
 }
 
+// The checks the paged-cache calls share; fills the kernels' views.
+static int check_paged(const qwen3_config& c, const char* what, int n_tokens, const qwen3_paged_batch* batch,
+                       const qwen3_kv_pages* kv, PagedBatch* pb, KvPages* pages) {
+  Q3_CHECK(batch && kv, QWEN3_EINVAL, "%s: batch or pages descriptor is NULL", what);
+  Q3_CHECK(batch->q_start && batch->ctx_len && batch->page_table, QWEN3_EINVAL,
+           "%s: batch->q_start / ctx_len / page_table is NULL", what);
+  Q3_CHECK(((reinterpret_cast<uintptr_t>(batch->q_start) | reinterpret_cast<uintptr_t>(batch->ctx_len) |
+             reinterpret_cast<uintptr_t>(batch->page_table)) & 3u) == 0,
+           QWEN3_EALIGN, "%s: the batch's int32 lists are not 4-byte aligned", what);
+  Q3_CHECK(n_tokens > 0 && batch->B > 0 && batch->max_pages > 0, QWEN3_EINVAL,
+           "%s: n_tokens (%d), batch->B (%d) and batch->max_pages (%d) must be positive", what, n_tokens, batch->B,
+           batch->max_pages);
+  Q3_CHECK(kv->k && kv->v, QWEN3_EINVAL, "%s: pages->k / pages->v is NULL", what);
+  Q3_CHECK(aligned16(kv->k) && aligned16(kv->v), QWEN3_EALIGN, "%s: pages are not 16-byte aligned", what);
+  Q3_CHECK(kv->fp8 == 0 || kv->fp8 == 1, QWEN3_EINVAL, "%s: pages->fp8 must be 0 or 1 (got %d)", what, kv->fp8);
+  if (kv->fp8) {
+    Q3_CHECK(kv->k_scale && kv->v_scale, QWEN3_EINVAL, "%s: e4m3 pages need k_scale and v_scale", what);
+    Q3_CHECK(((reinterpret_cast<uintptr_t>(kv->k_scale) | reinterpret_cast<uintptr_t>(kv->v_scale)) & 3u) == 0,
+             QWEN3_EALIGN, "%s: k_scale / v_scale are not 4-byte aligned", what);
+  }
+  int shift = -1;
+  for (int i = 4; i <= 8; ++i)
+    if (kv->page_size == 1 << i) shift = i;
+  Q3_CHECK(shift > 0, QWEN3_ESHAPE, "%s: page_size (%d) must be 16, 32, 64, 128 or 256", what, kv->page_size);
+  Q3_CHECK(kv->n_pages > 0, QWEN3_EINVAL, "%s: n_pages (%d) must be positive", what, kv->n_pages);
+  // cache rows and positions are 32-bit coordinates
+  Q3_CHECK((long long)kv->n_pages * c.n_kv_heads * kv->page_size < (1ll << 31) - 256, QWEN3_ESHAPE,
+           "%s: n_pages * n_kv_heads * page_size exceeds 2^31 rows", what);
+  Q3_CHECK((long long)batch->max_pages * kv->page_size < (1ll << 31) - 256, QWEN3_ESHAPE,
+           "%s: max_pages * page_size exceeds 2^31 positions", what);
+  pb->q_start = batch->q_start;
+  pb->ctx_len = batch->ctx_len;
+  pb->table = batch->page_table;
+  pb->B = batch->B;
+  pb->max_pages = batch->max_pages;
+  pages->k = static_cast<uint8_t*>(kv->k);
+  pages->v = static_cast<uint8_t*>(kv->v);
+  pages->k_scale = kv->k_scale;
+  pages->v_scale = kv->v_scale;
+  pages->n_pages = kv->n_pages;
+  pages->page_shift = shift;
+  pages->Hkv = c.n_kv_heads;
+  pages->fp8 = kv->fp8;
+  return 0;
+}
+
 static int finish(int rc) {
   if (rc == -6 && g_last_error.empty()) set_last_error("CUDA error: %s", cudaGetErrorString(cudaGetLastError()));
   return rc;
@@ -891,6 +948,7 @@ size_t qwen3_workspace_size(const qwen3_config* c, int op, int B, int T, int s_m
   if (!c || validate_cfg(c) != 0 || B <= 0 || s_max <= 0) return 0;
   if (op == QWEN3_OP_GENERATE)
     return T > 0 ? generate_stack_bytes(*c, B, T, s_max) + generate_extra_bytes(*c, B) : 0;
+  if (op == QWEN3_OP_ATTENTION_PAGED) return T > 0 ? paged_attention_bytes(B, c->n_q_heads, c->n_kv_heads, T) : 0;
   if (op < QWEN3_OP_BLOCK_PREFILL || op > QWEN3_OP_STACK_DECODE) return 0;
   if (op != QWEN3_OP_BLOCK_DECODE && op != QWEN3_OP_STACK_DECODE && T <= 0) return 0;
   return carve(*c, op, B, T, s_max, nullptr, nullptr);
@@ -1409,6 +1467,78 @@ int qwen3_op_attention_decode_noalloc(const qwen3_config* c, const qwen3_bf16* q
   return finish(launch_attention_decode_static(qkv, ldqkv, B, c->n_q_heads, c->n_kv_heads, cache_len, kv->k, kv->v,
                                                kv->s_max, o, ldo, device_error_word(),
                                                static_cast<cudaStream_t>(stream), c->gemm_f16 != 0));
+}
+
+int qwen3_op_qk_norm_rope_paged(const qwen3_config* c, const qwen3_bf16* qkv, long long ldqkv, int n_tokens,
+                                const qwen3_paged_batch* batch, const qwen3_bf16* q_norm, const qwen3_bf16* k_norm,
+                                const qwen3_kv_pages* kv, const float* rope, qwen3_bf16* q_out, long long ldq,
+                                void* stream) {
+  g_last_error.clear();
+  int rc = validate_cfg(c);
+  if (rc) return rc;
+  PagedBatch pb;
+  KvPages pages;
+  if ((rc = check_paged(*c, "qk_norm_rope_paged", n_tokens, batch, kv, &pb, &pages))) return rc;
+  Q3_CHECK(qkv && q_norm && k_norm && rope && q_out, QWEN3_EINVAL, "qk_norm_rope_paged: NULL pointer");
+  Q3_CHECK(aligned16(qkv) && aligned16(q_norm) && aligned16(k_norm) && aligned16(rope) && aligned16(q_out),
+           QWEN3_EALIGN, "qk_norm_rope_paged: misaligned pointer");
+  Q3_CHECK(ldqkv % 8 == 0 && ldqkv >= (long long)(c->n_q_heads + 2 * c->n_kv_heads) * c->head_dim, QWEN3_EALIGN,
+           "qk_norm_rope_paged: ldqkv (%lld) must be a multiple of 8 and cover the query, key and value heads", ldqkv);
+  Q3_CHECK(ldq % 8 == 0 && ldq >= (long long)c->n_q_heads * c->head_dim, QWEN3_EALIGN,
+           "qk_norm_rope_paged: ldq (%lld) must be a multiple of 8 and cover the query heads", ldq);
+  Q3_CHECK(q_out != qkv || ldq == ldqkv, QWEN3_EINVAL, "qk_norm_rope_paged: in place (q_out == qkv) needs ldq == ldqkv");
+  if ((rc = check_device())) return rc;
+  return finish(launch_qk_norm_rope_paged(qkv, ldqkv, n_tokens, pb, pages, c->n_q_heads, q_norm, k_norm, rope,
+                                          c->max_pos, c->rms_eps, q_out, ldq, device_error_word(),
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+int qwen3_op_attention_paged(const qwen3_config* c, const qwen3_bf16* q, long long ldq, int n_tokens, int max_q,
+                             const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, qwen3_bf16* o, long long ldo,
+                             void* ws, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  int rc = validate_cfg(c);
+  if (rc) return rc;
+  PagedBatch pb;
+  KvPages pages;
+  if ((rc = check_paged(*c, "attention_paged", n_tokens, batch, kv, &pb, &pages))) return rc;
+  Q3_CHECK(q && o && ws, QWEN3_EINVAL, "attention_paged: NULL pointer");
+  Q3_CHECK(aligned16(q) && aligned16(o) && aligned16(ws), QWEN3_EALIGN, "attention_paged: misaligned pointer");
+  Q3_CHECK(max_q > 0, QWEN3_EINVAL, "attention_paged: max_q (%d) must be positive", max_q);
+  const long long width = (long long)c->n_q_heads * c->head_dim;
+  Q3_CHECK(ldq % 8 == 0 && ldq >= width, QWEN3_EALIGN,
+           "attention_paged: ldq (%lld) must be a multiple of 8 and at least n_q_heads * head_dim (%lld)", ldq, width);
+  Q3_CHECK(ldo % 8 == 0 && ldo >= width, QWEN3_EALIGN,
+           "attention_paged: ldo (%lld) must be a multiple of 8 and at least n_q_heads * head_dim (%lld)", ldo, width);
+  const size_t need = paged_attention_bytes(pb.B, c->n_q_heads, c->n_kv_heads, max_q);
+  Q3_CHECK(ws_bytes >= need, QWEN3_EWORKSPACE, "attention_paged: workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if ((rc = check_device())) return rc;
+  return finish(launch_attention_paged(q, ldq, n_tokens, max_q, pb, pages, c->n_q_heads, ws, o, ldo,
+                                       device_error_word(), static_cast<cudaStream_t>(stream), c->gemm_f16 != 0));
+}
+
+static int kv_move(const qwen3_config* c, const char* what, bool to_pages, const qwen3_kv_layer* flat, int n_tokens,
+                   const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, void* stream) {
+  g_last_error.clear();
+  int rc = validate_cfg(c);
+  if (rc) return rc;
+  PagedBatch pb;
+  KvPages pages;
+  if ((rc = check_paged(*c, what, n_tokens, batch, kv, &pb, &pages))) return rc;
+  if ((rc = check_kv(*c, flat, 1))) return rc;
+  if ((rc = check_device())) return rc;
+  return finish(launch_kv_move(to_pages, flat->k, flat->v, flat->s_max, n_tokens, pb, pages, device_error_word(),
+                               static_cast<cudaStream_t>(stream)));
+}
+
+int qwen3_op_kv_to_pages(const qwen3_config* c, const qwen3_kv_layer* src, int n_tokens,
+                         const qwen3_paged_batch* batch, const qwen3_kv_pages* dst, void* stream) {
+  return kv_move(c, "kv_to_pages", true, src, n_tokens, batch, dst, stream);
+}
+
+int qwen3_op_kv_from_pages(const qwen3_config* c, const qwen3_kv_pages* src, int n_tokens,
+                           const qwen3_paged_batch* batch, const qwen3_kv_layer* dst, void* stream) {
+  return kv_move(c, "kv_from_pages", false, dst, n_tokens, batch, src, stream);
 }
 
 int qwen3_op_argmax(const float* x, long long ldx, int rows, int V, int* out, long long ld_out, void* stream) {

@@ -1,0 +1,280 @@
+// Writing and moving a paged KV cache: the per-head QK norm with the rotation and the
+// cache write of a ragged batch, and the copies between pages and a contiguous cache. All
+// of them are bound by the bytes they move; e4m3 pages quantise as they are written
+// (byte = e4m3(x / scale[head]), saturating) and widen as they are read (byte * scale).
+//
+// One scale per KV head, given by the caller: a key leaves its RMSNorm with a norm of at most
+// sqrt(128) max |w|, and e4m3 keeps its 3 mantissa bits over 15 binades, so a scale per
+// token would gain nothing; a scale per head folds into the attention's softmax factor and
+// epilogue.
+#include "paged.cuh"
+#include "internal.h"
+
+namespace q3 {
+
+namespace {
+
+// Rows of 128 values in flight per warp: 4 (token, head) rows at a time, 8 lanes each.
+constexpr int kSlotsPerWarp = 8;
+constexpr int kWarps = 8;
+
+struct NormRopeArgs {
+  PagedBatch pb;
+  KvPages kv;
+  const uint16_t* qkv;
+  long long ldqkv;
+  uint16_t* q_out;
+  long long ldq;
+  const uint16_t* qw;
+  const uint16_t* kw;
+  const float* rope;
+  int n_tokens, Hq, max_pos, n_blocks_tok;
+  float eps;
+  int* err;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+  f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+// x * inv as e4m3, 8 values
+__device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+}  // namespace
+
+// A group of 8 lanes owns one (token, head) row: lane l of the group holds dims [8l, 8l + 8)
+// and [64 + 8l, 64 + 8l + 8), so that the pairs of the rotation (i, i + 64) meet in one lane,
+// each load of 16 bytes is part of 128 contiguous ones, and the sum of squares takes three
+// shuffles. A warp owns kSlotsPerWarp consecutive head slots of a token.
+template <bool FP8>
+__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_paged_kernel(const NormRopeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int tok = (int)(item / a.n_blocks_tok);
+  if (tok >= a.n_tokens) return;
+  const int Hkv = a.kv.Hkv, slots = a.Hq + 2 * Hkv;
+  const int slot0 = (int)(item % a.n_blocks_tok) * kSlotsPerWarp + (lane >> 3);
+  const int d = (lane & 7) * 8;
+  constexpr int kIter = kSlotsPerWarp / 4;
+  uint4 lo[kIter], hi[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+    if (slot0 + 4 * i < slots) {
+      const uint16_t* row = a.qkv + tok * a.ldqkv + (long long)(slot0 + 4 * i) * 128;
+      lo[i] = *reinterpret_cast<const uint4*>(row + d);
+      hi[i] = *reinterpret_cast<const uint4*>(row + 64 + d);
+    }
+  }
+  const int b = paged_seq_of(a.pb, tok, lane);
+  if (b >= a.pb.B) return;  // a row behind the last sequence
+  const int t = tok - a.pb.q_start[b];
+  const int pos = a.pb.ctx_len[b] + t;
+  if (t < 0 || pos >= a.max_pos) {
+    if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
+    return;
+  }
+  const long long cell = paged_row(a.pb, a.kv, b, pos, lane == 0 ? a.err : nullptr);
+  if (cell < 0) return;
+  float cs[8], sn[8];
+  {
+    const float4* r = reinterpret_cast<const float4*>(a.rope + ((long long)pos * 64 + d) * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = r[i];
+      cs[2 * i] = v.x; sn[2 * i] = v.y; cs[2 * i + 1] = v.z; sn[2 * i + 1] = v.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int slot = slot0 + 4 * i;
+    float x[8], y[8];
+    unpack8(lo[i], x);
+    unpack8(hi[i], y);
+    const bool is_q = slot < a.Hq, is_v = slot >= a.Hq + Hkv;
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += x[j] * x[j] + y[j] * y[j];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (slot >= slots) continue;
+    if (!is_v) {
+      const float r = rsqrtf(ss * (1.0f / 128.0f) + a.eps);
+      const uint16_t* wn = is_q ? a.qw : a.kw;
+      float wx[8], wy[8];
+      unpack8(*reinterpret_cast<const uint4*>(wn + d), wx);
+      unpack8(*reinterpret_cast<const uint4*>(wn + 64 + d), wy);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = x[j] * r * wx[j], w = y[j] * r * wy[j];
+        x[j] = u * cs[j] - w * sn[j];
+        y[j] = u * sn[j] + w * cs[j];
+      }
+    }
+    if (is_q) {
+      uint16_t* dst = a.q_out + tok * a.ldq + (long long)slot * 128;
+      *reinterpret_cast<uint4*>(dst + d) = pack8(x);
+      *reinterpret_cast<uint4*>(dst + 64 + d) = pack8(y);
+      continue;
+    }
+    const int g = is_v ? slot - a.Hq - Hkv : slot - a.Hq;
+    const long long at = (cell + ((long long)g << a.kv.page_shift)) * 128 + d;
+    uint8_t* pool = is_v ? a.kv.v : a.kv.k;
+    if (FP8) {
+      const float inv = 1.0f / (is_v ? a.kv.v_scale : a.kv.k_scale)[g];
+      *reinterpret_cast<uint2*>(pool + at) = quant8(x, inv);
+      *reinterpret_cast<uint2*>(pool + at + 64) = quant8(y, inv);
+    } else {
+      *reinterpret_cast<uint4*>(pool + 2 * at) = is_v ? lo[i] : pack8(x);
+      *reinterpret_cast<uint4*>(pool + 2 * at + 128) = is_v ? hi[i] : pack8(y);
+    }
+  }
+}
+
+int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens, const PagedBatch& pb,
+                              const KvPages& kv, int Hq, const uint16_t* qw, const uint16_t* kw, const float* rope,
+                              int max_pos, float eps, uint16_t* q_out, long long ldq, int* err, cudaStream_t s) {
+  NormRopeArgs a;
+  a.pb = pb;
+  a.kv = kv;
+  a.qkv = qkv; a.ldqkv = ldqkv;
+  a.q_out = q_out; a.ldq = ldq;
+  a.qw = qw; a.kw = kw; a.rope = rope;
+  a.n_tokens = n_tokens; a.Hq = Hq; a.max_pos = max_pos;
+  a.n_blocks_tok = (Hq + 2 * kv.Hkv + kSlotsPerWarp - 1) / kSlotsPerWarp;
+  a.eps = eps;
+  a.err = err;
+  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
+  if (blocks >= (1ll << 31)) {
+    set_last_error("qk_norm_rope_paged: %d tokens exceed the grid limit", n_tokens);
+    return -2;
+  }
+  q3_launch(kv.fp8 ? qk_norm_rope_paged_kernel<true> : qk_norm_rope_paged_kernel<false>, (unsigned)blocks,
+            32 * kWarps, 0, s, a);
+  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+}
+
+// ---------------------------------------------------------------------------
+// Copies between pages and a contiguous cache [B][Hkv][s_max][128] bf16: the batch's new
+// positions of every head, k and v. 16 lanes per row of 128 values (16 bytes of bf16, 8 of
+// e4m3, a lane), 8 rows in flight per warp: the 2 Hkv rows of a token go to ceil(2 Hkv / 8)
+// warps.
+// ---------------------------------------------------------------------------
+namespace {
+struct MoveArgs {
+  PagedBatch pb;
+  KvPages kv;
+  uint16_t* ck;
+  uint16_t* cv;
+  int s_max, n_tokens, n_blocks_tok;
+  int* err;
+};
+}  // namespace
+
+template <bool FP8, bool TO_PAGES>
+__global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int tok = (int)(item / a.n_blocks_tok);
+  if (tok >= a.n_tokens) return;
+  const int Hkv = a.kv.Hkv;
+  const int b = paged_seq_of(a.pb, tok, lane);
+  if (b >= a.pb.B) return;
+  const int t = tok - a.pb.q_start[b];
+  const int pos = a.pb.ctx_len[b] + t;
+  if (t < 0 || pos >= a.s_max) {
+    if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
+    return;
+  }
+  const long long cell = paged_row(a.pb, a.kv, b, pos, lane == 0 ? a.err : nullptr);
+  if (cell < 0) return;
+  const int row0 = (int)(item % a.n_blocks_tok) * 8 + (lane >> 4);
+  const int d = (lane & 15) * 8;
+  uint4 in[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 2 * i;
+    if (r >= 2 * Hkv) continue;
+    const bool is_v = r >= Hkv;
+    const int h = is_v ? r - Hkv : r;
+    const long long flat = ((long long)b * Hkv + h) * a.s_max + pos;
+    const long long paged = cell + ((long long)h << a.kv.page_shift);
+    if (TO_PAGES) {
+      in[i] = *reinterpret_cast<const uint4*>((is_v ? a.cv : a.ck) + flat * 128 + d);
+    } else if (FP8) {
+      const uint2 u = *reinterpret_cast<const uint2*>((is_v ? a.kv.v : a.kv.k) + paged * 128 + d);
+      in[i] = make_uint4(u.x, u.y, 0, 0);
+    } else {
+      in[i] = *reinterpret_cast<const uint4*>((is_v ? a.kv.v : a.kv.k) + (paged * 128 + d) * 2);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 2 * i;
+    if (r >= 2 * Hkv) continue;
+    const bool is_v = r >= Hkv;
+    const int h = is_v ? r - Hkv : r;
+    const long long flat = ((long long)b * Hkv + h) * a.s_max + pos;
+    const long long paged = cell + ((long long)h << a.kv.page_shift);
+    uint8_t* pool = is_v ? a.kv.v : a.kv.k;
+    uint16_t* cont = is_v ? a.cv : a.ck;
+    if (FP8) {
+      const float scale = (is_v ? a.kv.v_scale : a.kv.k_scale)[h];
+      float f[8];
+      if (TO_PAGES) {
+        unpack8(in[i], f);
+        *reinterpret_cast<uint2*>(pool + paged * 128 + d) = quant8(f, 1.0f / scale);
+      } else {
+        const uint32_t w[2] = {in[i].x, in[i].y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = e4m3x2_to_f32x2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+          f[2 * j] = p.x * scale;
+          f[2 * j + 1] = p.y * scale;
+        }
+        *reinterpret_cast<uint4*>(cont + flat * 128 + d) = pack8(f);
+      }
+    } else if (TO_PAGES) {
+      *reinterpret_cast<uint4*>(pool + (paged * 128 + d) * 2) = in[i];
+    } else {
+      *reinterpret_cast<uint4*>(cont + flat * 128 + d) = in[i];
+    }
+  }
+}
+
+int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_tokens, const PagedBatch& pb,
+                   const KvPages& kv, int* err, cudaStream_t s) {
+  MoveArgs a;
+  a.pb = pb;
+  a.kv = kv;
+  a.ck = ck;
+  a.cv = cv;
+  a.s_max = s_max;
+  a.n_tokens = n_tokens;
+  a.n_blocks_tok = (2 * kv.Hkv + 7) / 8;
+  a.err = err;
+  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
+  if (blocks >= (1ll << 31)) {
+    set_last_error("kv move: %d tokens exceed the grid limit", n_tokens);
+    return -2;
+  }
+  auto k = to_pages ? (kv.fp8 ? kv_move_kernel<true, true> : kv_move_kernel<false, true>)
+                    : (kv.fp8 ? kv_move_kernel<true, false> : kv_move_kernel<false, false>);
+  q3_launch(k, (unsigned)blocks, 32 * kWarps, 0, s, a);
+  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+}
+
+}  // namespace q3
