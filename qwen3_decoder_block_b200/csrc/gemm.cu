@@ -974,10 +974,14 @@ int encode_cached(CUtensorMap* map, const TmapKey& k) {
   if (!enc) return -1;
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r =
-      enc(map, k.kind == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k.rank,
+      enc(map,
+          k.kind == 1   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+          : k.kind == 3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+          k.rank,
           const_cast<void*>(k.base), k.dims, k.strides, k.box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
           k.kind == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-          k.kind == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+          k.kind == 0 || k.kind == 3 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return -2;
   std::lock_guard<std::mutex> lk(g_tmap_mu);
@@ -1008,6 +1012,21 @@ int make_tmap_2d(CUtensorMap* map, const void* base, long long rows, long long c
   k.dims[1] = (cuuint64_t)rows;
   k.strides[0] = (cuuint64_t)(ld * 2);
   k.box[0] = 64;
+  k.box[1] = (cuuint32_t)box_rows;
+  return encode_cached(map, k);
+}
+
+// Tensor map over rows of 128 bytes (row stride ld bytes), box = box_rows whole rows, 128-byte
+// swizzle, zero fill out of bounds.
+int make_tmap_bytes(CUtensorMap* map, const void* base, long long rows, long long ld, int box_rows) {
+  TmapKey k = {};
+  k.kind = 3;
+  k.rank = 2;
+  k.base = base;
+  k.dims[0] = 128;
+  k.dims[1] = (cuuint64_t)rows;
+  k.strides[0] = (cuuint64_t)ld;
+  k.box[0] = 128;
   k.box[1] = (cuuint32_t)box_rows;
   return encode_cached(map, k);
 }
