@@ -159,30 +159,31 @@ __global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const P
 // two e4m3 terms (exact for bf16 queries) and P as three, each 16 times finer than the last
 // (P scaled so that the running maximum is 2^5 to 2^8 of e4m3's 448: relative error 2^-12, or
 // 2^-23 of the row's largest weight, finer than bf16), in columns [t G, t G + G) of term t.
-// A TMA warp fills a ring of tiles, one box per page (16-row boxes in a row's last tile, so
-// that no page past the last key is touched); its lanes look the next tile's pages up while
-// the ring is full. One warp issues S, one P.V; softmax warps own one key (S) and one head
-// dim (O) a thread. A row that spans CTAs leaves partials; the last of them to arrive merges
+// Two TMA warps fill rings of K and of V tiles, one box per page; one warp issues S, one P.V; two sets of softmax warps take alternate tiles,
+// a thread owning one key (S) and one head dim (O). A row that spans CTAs leaves partials; the last of them to arrive merges
 // them in CTA order, so the result does not depend on which one that is, and nobody waits.
 // ============================================================================
 template <int G, bool FP8>
 struct DecodeCfg {
   static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 1;
   static constexpr int kCols = (kPTerms * G + 15) / 16 * 16;          // MMA N
-  static constexpr int kHeadWarps = G >= 8 ? 4 : (G >= 2 ? 2 : 1);    // softmax warps per lane quarter
-  static constexpr int kSoftmaxWarps = 4 * kHeadWarps;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+  static constexpr int kHeadWarps = G >= 8 ? 2 : 1;                   // softmax warps of a set per lane quarter
+  static constexpr int kSetWarps = 4 * kHeadWarps;
+  static constexpr int kSoftmaxWarps = 2 * kSetWarps;                 // set X takes the CTA's tiles of parity X
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kStages = FP8 ? 5 : 3;
   static constexpr uint32_t kKV = FP8 ? kTile8 : 2 * kTile8;          // K or V of one tile
   static constexpr uint32_t kQB = (FP8 ? 1 : 2) * kCols * 128;        // q rows of one tile
-  static constexpr uint32_t kOffV = kKV, kOffQ = 2 * kKV;
-  static constexpr uint32_t kStage = 2 * kKV + kQB;
+  static constexpr uint32_t kStage = kKV + kQB;                       // K ring: a tile and its q rows; V ring: kKV
+  static constexpr uint32_t kOffV = kStages * kStage;
   static constexpr uint32_t kPB = (FP8 ? 1 : 2) * kCols * 128;        // one P buffer
-  static constexpr uint32_t kOffP = kStages * kStage;
-  static constexpr uint32_t kOffRed = kOffP + 2 * kPB;                // maxima [2][4][16], sums [4][16]
-  static constexpr uint32_t kOffBar = kOffRed + 3 * 64 * 4;
-  static constexpr uint32_t kSmem = kOffBar + (2 * kStages + 10) * 8 + 16 + 1024;
-  static constexpr uint32_t kTmem = 3 * kCols <= 64 ? 64 : (3 * kCols <= 128 ? 128 : 256);
+  static constexpr uint32_t kOffP = kOffV + kStages * kKV;
+  static constexpr uint32_t kOffRed = kOffP + 2 * kPB;                // per set: maxima [2][4][16], sums [4][16]
+  static constexpr uint32_t kOffX = kOffRed + 2 * 3 * 64 * 4;         // set 1's row: o [G][128], m [16], l [16]
+  static constexpr uint32_t kOffBar = kOffX + G * kD * 4 + 2 * 16 * 4;
+  static constexpr uint32_t kSmem = kOffBar + (4 * kStages + 10) * 8 + 16 + 1024;
+  // tensor memory: S of set 0 and 1, O of set 0 and 1
+  static constexpr uint32_t kTmem = 4 * kCols <= 64 ? 64 : (4 * kCols <= 128 ? 128 : 256);
 };
 
 // Walk over the (sequence, group) rows that meet this CTA's tiles.
@@ -218,8 +219,16 @@ struct RowWalk {
   }
 };
 
-template <int N>
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+// One arrival for a warp, once all its lanes are here (32 arrivals on one barrier would queue
+// up at one shared-memory word).
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void named_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 // Element base + hh * GH + jj of a register array for the warp's head group hh (run time)
 // and head jj (a constant after unrolling): constant indices keep the array in registers.
@@ -278,30 +287,30 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
                              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
                              const __grid_constant__ CUtensorMap tmV16, const PagedAttn a) {
   using C = DecodeCfg<G, FP8>;
-  constexpr int SW = C::kSoftmaxWarps, HW = C::kHeadWarps, GH = G / HW, NC = C::kCols, NS = C::kStages;
+  constexpr int SW = C::kSoftmaxWarps, XW = C::kSetWarps, HW = C::kHeadWarps, GH = G / HW, NC = C::kCols, NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] stage loaded
-  uint64_t* empty = full + NS;                                      // [NS] stage consumed
-  uint64_t* s_full = empty + NS;   // [2] scores ready
-  uint64_t* s_empty = s_full + 2;  // [2] scores read
-  uint64_t* p_full = s_full + 4;   // [2] P buffer written (and O rescaled)
-  uint64_t* pv_done = s_full + 6;  // [2] P.V of a tile using that buffer complete
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] K (and q) loaded
+  uint64_t* k_empty = k_full + NS;                                    // [NS] ... consumed
+  uint64_t* v_full = k_full + 2 * NS;                                 // [NS] V loaded
+  uint64_t* v_empty = k_full + 3 * NS;                                // [NS] ... consumed
+  uint64_t* s_full = k_full + 4 * NS;  // [2] scores of set X ready
+  uint64_t* s_empty = s_full + 2;  // [2] scores of set X read
+  uint64_t* p_full = s_full + 4;   // [2] P of set X written (and its O rescaled)
+  uint64_t* pv_done = s_full + 6;  // [2] P.V of set X's tile complete
   uint64_t* drain = s_full + 8;    // [2] an issuer's MMAs complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 10);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_b0 = s_abort + 1;    // sequence holding this CTA's first tile
   volatile int* s_last = s_abort + 2;  // this CTA merges the row
-  float* red_max = reinterpret_cast<float*>(smem + C::kOffRed);  // [2][4][16]
-  float* red_sum = red_max + 2 * 64;                             // [4][16]
   int* err = a.err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 4 * NS; ++i) mbar_init(&k_full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 32 * SW);
-      mbar_init(&p_full[i], 32 * SW); mbar_init(&pv_done[i], 1); mbar_init(&drain[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], XW);
+      mbar_init(&p_full[i], XW); mbar_init(&pv_done[i], 1); mbar_init(&drain[i], 1);
     }
     *s_abort = 0;
     *s_b0 = 0;
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   // Unused rows of the Q and P operand tiles are never written: clear all of them once.
   for (int i = threadIdx.x; i < (int)((NS * C::kQB + 2 * C::kPB) / 16); i += blockDim.x) {
     const uint32_t off = 16u * i;
-    uint8_t* p = off < NS * C::kQB ? smem + (off / C::kQB) * C::kStage + C::kOffQ + off % C::kQB
+    uint8_t* p = off < NS * C::kQB ? smem + (off / C::kQB) * C::kStage + C::kKV + off % C::kQB
                                    : smem + C::kOffP + (off - NS * C::kQB);
     *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
   }
@@ -336,88 +345,105 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   __syncthreads();
   const int b0 = *s_b0;
 
-  if (warp == SW) {
-    // -------------------------------------------------------------------- TMA producer
-    // Boxes of a tile: 128 / rows of them, rows = min(page, 128) keys each (16 in a row's last
-    // tile); parts K, V of e4m3 pages, or K lo / K hi / V lo / V hi halves of 64 dims of bf16
-    // ones. Lane l issues box l % n of part l / n.
-    constexpr int kParts = FP8 ? 2 : 4;
-    const int box = min(1 << a.kv.page_shift, kTileK);
-    const long long rows_all = ((long long)a.kv.n_pages * Hkv) << a.kv.page_shift;
+  if (warp == SW || warp == SW + 3) {
+    // -------------------------------------------------- TMA producers: K and q; V
+    // One box per page of a tile, min(page, 128) keys each (16 in a row's last tile, so that
+    // nothing past its last 16 keys is read), twice for the two 64-dim halves of bf16. Lane i
+    // looks up the page of box i, a tile ahead: the load lands while the ring is full.
+    const bool is_v = warp == SW + 3;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    const CUtensorMap* map16 = is_v ? &tmV16 : &tmK16;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    const uint32_t ring = is_v ? C::kOffV : 0, stage = is_v ? C::kKV : C::kStage;
+    const int shift = a.kv.page_shift, box_shift = min(shift, 7);
+    const int rows_all = (int)(((long long)a.kv.n_pages * Hkv) << shift);
     RowWalk w(a, b0, t_begin, t_end);
-    int j = w.valid() ? w.j0() : 0;
-    // the page of this lane's box in tile jj of row ww (-1: no box)
-    auto lane_page = [&](const RowWalk& ww, int jj, int* rows) {
-      const int left = ww.n_keys - jj * kTileK;
-      *rows = left >= kTileK ? box : 16;
-      const int n = left >= kTileK ? kTileK / box : (left + 15) / 16;
-      if (lane >= n * kParts) return -1;
-      const int p = (jj * kTileK + (lane % n) * *rows) >> a.kv.page_shift;
-      return __ldg(a.pb.table + (long long)ww.b * a.pb.max_pages + p);
+    int j = w.valid() ? w.j0() : 0, je = w.valid() ? w.j1() : 0;
+    // the page of this lane's box in tile j of row w
+    auto lane_page = [&]() {
+      const int left = w.n_keys - j * kTileK;
+      const int bs = left >= kTileK ? box_shift : 4;
+      const int key = j * kTileK + (lane << bs);
+      if (lane >= (kTileK >> bs) || key >= w.n_keys) return -1;
+      return __ldg(a.pb.table + (long long)w.b * a.pb.max_pages + (key >> shift));
     };
-    int rows = 16, page = w.valid() ? lane_page(w, j, &rows) : -1;
-    long long tc = 0;
+    int page = w.valid() ? lane_page() : -1;
+    int st = 0, n_tiles = 0;
+    uint32_t phase = 0;
     bool ok = true;
     while (w.valid()) {
       const int b = w.b, g = w.g, k0 = j * kTileK, left = w.n_keys - k0;
-      const int cur_rows = rows, cur_page = page;
-      if (++j >= w.j1()) {
+      const int cur_page = page;
+      if (++j >= je) {
         w.next();
-        j = w.valid() ? w.j0() : 0;
+        if (w.valid()) {
+          j = w.j0();
+          je = w.j1();
+        }
       }
-      if (w.valid()) page = lane_page(w, j, &rows);  // lands while this tile waits for its stage
-      const int st = (int)(tc % NS);
-      ok = !*s_abort && mbar_wait(&empty[st], (uint32_t)((tc / NS) & 1) ^ 1u, err);
+      if (w.valid()) page = lane_page();
+      ok = !*s_abort && mbar_wait(&empty[st], phase ^ 1u, err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      uint8_t* base = smem + st * C::kStage;
-      const int n = left >= kTileK ? kTileK / box : (left + 15) / 16;
-      const int tok = FP8 ? 0 : a.pb.q_start[b];
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], n * cur_rows * 128 * kParts + C::kQTerms * G * 128 * (FP8 ? 1 : 2));
-        if (FP8) {
-          tma_load_2d(base + C::kOffQ, &tmQ, &full[st], 0, (b * Hkv + g) * 2 * G);
-        } else {
-          tma_load_3d(base + C::kOffQ, &tmQ, &full[st], 0, g * G, tok);
-          tma_load_3d(base + C::kOffQ + NC * 128, &tmQ, &full[st], 64, g * G, tok);
+      uint8_t* base = smem + ring + st * stage;
+      const bool tail = left < kTileK;
+      const int bs = tail ? 4 : box_shift;
+      const int n = tail ? (left + 15) >> 4 : kTileK >> bs;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[st], (n << bs) * 128 * (FP8 ? 1 : 2) +
+                                             (is_v ? 0 : C::kQTerms * G * 128 * (FP8 ? 1 : 2)));
+        if (!is_v) {
+          if (FP8) {
+            tma_load_2d(base + C::kKV, &tmQ, &full[st], 0, (b * Hkv + g) * 2 * G);
+          } else {
+            const int tok = a.pb.q_start[b];
+            tma_load_3d(base + C::kKV, &tmQ, &full[st], 0, g * G, tok);
+            tma_load_3d(base + C::kKV + NC * 128, &tmQ, &full[st], 64, g * G, tok);
+          }
         }
       }
       __syncwarp();
-      if (lane < n * kParts) {
-        const int i = lane % n, part = lane / n;
-        const bool bad = cur_page < 0 || cur_page >= a.kv.n_pages;
-        if (bad) record_error(err, kErrInvalid);
-        const int slot = (k0 + i * cur_rows) & ((1 << a.kv.page_shift) - 1);
-        // a bad page reads as zeros: its rows lie behind the tensor map's last one
-        const int row = bad ? (int)rows_all : (int)((((long long)cur_page * Hkv + g) << a.kv.page_shift) + slot);
-        const bool is_v = part >= kParts / 2;
-        const bool tail = left < kTileK;
-        const CUtensorMap* m = is_v ? (tail ? &tmV16 : &tmV) : (tail ? &tmK16 : &tmK);
-        const int half = FP8 ? 0 : part & 1;
-        tma_load_2d(base + (is_v ? C::kOffV : 0) + half * kTile8 + i * cur_rows * 128, m, &full[st], 64 * half, row);
+      if (lane < n && (cur_page < 0 || cur_page >= a.kv.n_pages)) record_error(err, kErrInvalid);
+      const CUtensorMap* m = tail ? map16 : map;
+      for (int i = 0; i < n; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, cur_page, i);
+        // a bad page reads as zeros: behind the tensor map's last row
+        const int row = pg < 0 || pg >= a.kv.n_pages
+                            ? rows_all
+                            : ((pg * Hkv + g) << shift) + ((k0 + (i << bs)) & ((1 << shift) - 1));
+        uint8_t* dst = base + ((i << bs) * 128);
+        if (elect_one()) {
+          tma_load_2d(dst, m, &full[st], 0, row);
+          if (!FP8) tma_load_2d(dst + kTile8, m, &full[st], 64, row);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      ++tc;
+      ++n_tiles;
+      if (++st == NS) { st = 0; phase ^= 1u; }
     }
     if (!ok) {
       *s_abort = 1;
       // let the copies still in flight land before the CTA exits
-      for (long long i = tc > NS ? tc - NS : 0; i < tc; ++i) mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), err);
+      for (int i = n_tiles > NS ? n_tiles - NS : 0; i < n_tiles; ++i)
+        mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), err);
     }
   } else if (warp == SW + 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ S issuer: S = K q
       constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 0, 0) : idesc_bf16_f32(128, NC, 0, 0);
-      const long long n_tiles = t_end - t_begin;
+      const int n_tiles = (int)(t_end - t_begin);
+      int st = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      for (long long tc = 0; tc < n_tiles && ok; ++tc) {
-        const int st = (int)(tc % NS), sb = (int)(tc & 1);
-        if (*s_abort || !mbar_wait(&full[st], (uint32_t)((tc / NS) & 1), err)) { ok = false; break; }
+      for (int tc = 0; tc < n_tiles && ok; ++tc) {
+        const int sb = tc & 1;
+        if (*s_abort || !mbar_wait(&k_full[st], phase, err)) { ok = false; break; }
         if (tc >= 2 && (*s_abort || !mbar_wait(&s_empty[sb], (uint32_t)(((tc - 2) >> 1) & 1), err))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sK = smem_u32(smem + st * C::kStage), sQ = sK + C::kOffQ;
+        const uint32_t sK = smem_u32(smem + st * C::kStage), sQ = sK + C::kKV;
         if (FP8) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -430,6 +456,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
                         sdesc_kmajor_sw128(sQ + (kk >> 2) * NC * 128) + 2 * (kk & 3), idesc, kk ? 1u : 0u);
         }
         mma_commit(&s_full[sb]);
+        mma_commit(&k_empty[st]);
+        if (++st == NS) { st = 0; phase ^= 1u; }
       }
       if (!ok) *s_abort = 1;
       mma_commit(&drain[0]);  // every MMA completes before the tensor memory is released
@@ -437,36 +465,38 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     }
   } else if (warp == SW + 2) {
     if (lane == 0) {
-      // -------------------------------------------- P.V issuer: O^T += V^T P^T, stage release
+      // -------------------------------------------- P.V issuer: O^T += V^T P^T
       constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 1, 0) : idesc_bf16_f32(128, NC, 1, 0);
-      long long tc = 0;
+      int tc = 0, st = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (RowWalk w(a, b0, t_begin, t_end); w.valid() && ok; w.next()) {
         const int jb = w.j0(), je = w.j1();
         for (int j = jb; j < je; ++j, ++tc) {
-          const int st = (int)(tc % NS), pb = (int)(tc & 1);
-          if (*s_abort || !mbar_wait(&full[st], (uint32_t)((tc / NS) & 1), err) ||
+          const int pb = tc & 1;
+          if (*s_abort || !mbar_wait(&v_full[st], phase, err) ||
               !mbar_wait(&p_full[pb], (uint32_t)((tc >> 1) & 1), err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sV = smem_u32(smem + st * C::kStage + C::kOffV);
-          const uint32_t sP = smem_u32(smem + C::kOffP + pb * C::kPB);
+          const uint32_t sV = smem_u32(smem + C::kOffV + st * C::kKV);
+          const uint32_t sP = smem_u32(smem + C::kOffP + pb * C::kPB), tO = tmO + pb * NC;
           if (FP8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 keys an instruction
-              mma_e4m3_ss(tmO, sdesc_mnmajor_sw128(sV + kk * 32 * 128, kTile8, 1024), sdesc_kmajor_sw128(sP) + 2 * kk,
-                          idesc, (j == jb && kk == 0) ? 0u : 1u);
+              mma_e4m3_ss(tO, sdesc_mnmajor_sw128(sV + kk * 32 * 128, kTile8, 1024), sdesc_kmajor_sw128(sP) + 2 * kk,
+                          idesc, (j < jb + 2 && kk == 0) ? 0u : 1u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 keys an instruction
-              mma_bf16_ss(tmO, sdesc_mnmajor_sw128(sV + kk * 16 * 128, kTile8, 1024),
+              mma_bf16_ss(tO, sdesc_mnmajor_sw128(sV + kk * 16 * 128, kTile8, 1024),
                           sdesc_kmajor_sw128(sP + (kk >> 2) * NC * 128) + 2 * (kk & 3), idesc,
-                          (j == jb && kk == 0) ? 0u : 1u);
+                          (j < jb + 2 && kk == 0) ? 0u : 1u);
           }
           mma_commit(&pv_done[pb]);
-          mma_commit(&empty[st]);
+          mma_commit(&v_empty[st]);
+          if (++st == NS) { st = 0; phase ^= 1u; }
         }
       }
       if (!ok) *s_abort = 1;
@@ -475,15 +505,24 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------- softmax
-    // warp (quarter qd, half hh): key / head dim t of lanes [32 qd, 32 qd + 32), heads
-    // [j0, j0 + GH) of the group
-    const int qd = warp & 3, hh = warp >> 2, j0 = hh * GH;
+    // warp (set X, quarter qd, half hh): key / head dim t of lanes [32 qd, 32 qd + 32), heads
+    // [j0, j0 + GH) of the group, the CTA's tiles of parity X. Two sets, each with its own S,
+    // P, O, maxima and sums, keep two tiles' softmax chains in flight (one chain takes longer
+    // than an e4m3 tile's share of the memory bandwidth); a row's two halves meet at its end.
+    const int X = warp / XW, qd = warp & 3, hh = (warp % XW) >> 2, j0 = hh * GH;
     const int t = qd * 32 + lane;
     const uint32_t lanes = (uint32_t)(qd * 32) << 16;
+    const uint32_t tS = tmem + lanes + NC * X, tO = tmO + lanes + NC * X;
+    float* red_max = reinterpret_cast<float*>(smem + C::kOffRed) + X * 3 * 64;  // [2][4][16]
+    float* red_sum = red_max + 2 * 64;                                          // [4][16]
+    float* x_o = reinterpret_cast<float*>(smem + C::kOffX);                     // [G][128]
+    float* x_ml = x_o + G * kD;                                                 // m [16], l [16]
+    uint8_t* p_buf = smem + C::kOffP + X * C::kPB;
     // e4m3: the running maximum is kept 5 below the scores', so that P lies in (0, 2^8]
     constexpr float kShift = FP8 ? 5.f : 0.f;
     constexpr int kSCols = (C::kQTerms * G + 15) / 16 * 16;
-    long long tc = 0;
+    int tc0 = 0;  // the CTA's tiles before the current row
+    int u = 0;    // the set's tiles so far
     bool ok = true;
     for (RowWalk w(a, b0, t_begin, t_end); w.valid(); w.next()) {
       const int b = w.b, g = w.g, bg = b * Hkv + g;
@@ -495,20 +534,21 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         m_run[jj] = -INFINITY;
         l_part[jj] = 0.f;
       }
-      for (int j = jb; j < je; ++j, ++tc) {
+      const int j_first = jb + ((tc0 ^ X) & 1);
+      for (int j = j_first; j < je; j += 2, ++u) {
         const int nk = min(kTileK, w.n_keys - j * kTileK);
-        const int sb = (int)(tc & 1);
-        ok = ok && !*s_abort && mbar_wait(&s_full[sb], (uint32_t)((tc >> 1) & 1), err);
+        const uint32_t par = (uint32_t)(u & 1);
+        ok = ok && !*s_abort && mbar_wait(&s_full[X], par, err);
         ok = __all_sync(0xffffffffu, ok);
         uint32_t sv[kSCols];
 #pragma unroll
         for (int i = 0; i < kSCols; ++i) sv[i] = 0u;
         if (ok) {
           tc_fence_after();
-          tmem_ld_cols<kSCols>(tmem + lanes + NC * sb, sv);
+          tmem_ld_cols<kSCols>(tS, sv);
         }
         tc_fence_before();
-        mbar_arrive(&s_empty[sb]);
+        arrive_warp(&s_empty[X], lane);
         float s[GH];
 #pragma unroll
         for (int jj = 0; jj < GH; ++jj) {
@@ -517,12 +557,12 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           s[jj] = (ok && t < nk) ? x * factor[jj] : -INFINITY;
         }
         // tile maximum per head: the warp's 32 keys, then the 4 quarters
-        float* rm = red_max + (tc & 1) * 64;
+        float* rm = red_max + par * 64;
         {
           const float wm = reduce_heads<GH, true>(s, lane);
           if ((lane & (32 / GH - 1)) == 0) rm[qd * 16 + j0 + lane / (32 / GH)] = wm;
         }
-        softmax_bar<32 * SW>();
+        named_bar(1 + X, 32 * XW);
         float alpha[GH], p[GH];
         bool rescale = false;
 #pragma unroll
@@ -538,34 +578,26 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           p[jj] = (t < nk && m_run[jj] != -INFINITY) ? ex2_approx(s[jj] - m_run[jj]) : 0.f;
           l_part[jj] = l_part[jj] * alpha[jj] + p[jj];
         }
-        // P buffer tc & 1 was last read by the P.V of tile tc - 2; a rescale of O needs the
-        // P.V of tile tc - 1 complete as well
-        const int pbuf = (int)(tc & 1);
-        if (tc >= 2) {
-          ok = ok && !*s_abort && mbar_wait(&pv_done[pbuf], (uint32_t)(((tc - 2) >> 1) & 1), err);
-          ok = __all_sync(0xffffffffu, ok);
-        }
-        if (j > jb && rescale) {  // uniform within the warp: its lanes hold the same maxima
-          ok = ok && !*s_abort && mbar_wait(&pv_done[pbuf ^ 1], (uint32_t)(((tc - 1) >> 1) & 1), err);
+        // the set's P buffer and O are free once the P.V of its previous tile is complete
+        if (u >= 1) {
+          ok = ok && !*s_abort && mbar_wait(&pv_done[X], par ^ 1u, err);
           ok = __all_sync(0xffffffffu, ok);
         }
         if (ok) {
           tc_fence_after();
-          if (j > jb && rescale) {
+          if (j > j_first && rescale) {  // uniform within the warp: its lanes hold the same maxima
             uint32_t ov[NC];
-            tmem_ld_cols<NC>(tmO + lanes, ov);
+            tmem_ld_cols<NC>(tO, ov);
 #pragma unroll
             for (int term = 0; term < C::kPTerms; ++term)
 #pragma unroll
               for (int jj = 0; jj < GH; ++jj)
-                tmem_st1(tmO + lanes + term * G + j0 + jj,
-                         __float_as_uint(pick<HW, GH>(ov, term * G, hh, jj) * alpha[jj]));
+                tmem_st1(tO + term * G + j0 + jj, __float_as_uint(pick<HW, GH>(ov, term * G, hh, jj) * alpha[jj]));
             tmem_wait_st();
           }
           // P[row][t] into the K-major B tile: row term * G + head, 128-byte swizzle
-          uint8_t* pb = smem + C::kOffP + pbuf * C::kPB;
           if (FP8) {
-            pb += t & 15;
+            uint8_t* pb = p_buf + (t & 15);
 #pragma unroll
             for (int jj = 0; jj < GH; jj += 2) {
               float r0 = p[jj], r1 = jj + 1 < GH ? p[jj + 1 < GH ? jj + 1 : jj] : 0.f;
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
               }
             }
           } else {
-            pb += (t >> 6) * NC * 128 + (t & 7) * 2;
+            uint8_t* pb = p_buf + (t >> 6) * NC * 128 + (t & 7) * 2;
             const int chunk = (t & 63) >> 3;
 #pragma unroll
             for (int jj = 0; jj < GH; ++jj) {
@@ -592,34 +624,42 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
             }
           }
           // keys past the last one: zero their V rows (0 * NaN would poison O)
-          if (hh == 0 && t >= nk) {
-            uint4* v = reinterpret_cast<uint4*>(smem + (int)(tc % NS) * C::kStage + C::kOffV + t * 128);
+          if (hh == 0 && nk < kTileK) {
+            const int tc = tc0 + (j - jb), st = tc % NS;
+            ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (uint32_t)((tc / NS) & 1), err));
+            if (ok && t >= nk) {
+              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kKV + t * 128);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              v[c] = make_uint4(0, 0, 0, 0);
-              if (!FP8) v[c + kTile8 / 16] = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < 8; ++c) {
+                v[c] = make_uint4(0, 0, 0, 0);
+                if (!FP8) v[c + kTile8 / 16] = make_uint4(0, 0, 0, 0);
+              }
             }
           }
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[pbuf]);
+        arrive_warp(&p_full[X], lane);
       }
+      tc0 += je - jb;
       // end of the row's tiles in this CTA: O from tensor memory, the sums of the quarters
+      const bool any = j_first < je;
       uint32_t ov[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) ov[i] = 0u;
-      ok = ok && !*s_abort && mbar_wait(&pv_done[(tc - 1) & 1], (uint32_t)(((tc - 1) >> 1) & 1), err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after();
-        tmem_ld_cols<NC>(tmO + lanes, ov);
+      if (any) {
+        ok = ok && !*s_abort && mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_cols<NC>(tO, ov);
+        }
       }
       {
         const float ws = reduce_heads<GH, false>(l_part, lane);
         if ((lane & (32 / GH - 1)) == 0) red_sum[qd * 16 + j0 + lane / (32 / GH)] = ws;
       }
-      softmax_bar<32 * SW>();
+      named_bar(1 + X, 32 * XW);
       float o[GH], l[GH];
 #pragma unroll
       for (int jj = 0; jj < GH; ++jj) {
@@ -631,6 +671,31 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         }
         l[jj] = red_sum[hd] + red_sum[16 + hd] + red_sum[32 + hd] + red_sum[48 + hd];
       }
+      // set 1 hands its half of the row to set 0, which carries on with the whole
+      if (X == 1) {
+#pragma unroll
+        for (int jj = 0; jj < GH; ++jj) {
+          x_o[(j0 + jj) * kD + t] = o[jj];
+          if (t == jj) {
+            x_ml[j0 + jj] = m_run[jj];
+            x_ml[16 + j0 + jj] = l[jj];
+          }
+        }
+      }
+      named_bar(3, 32 * SW);
+      if (X == 0) {
+#pragma unroll
+        for (int jj = 0; jj < GH; ++jj) {
+          const int hd = j0 + jj;
+          const float m1 = x_ml[hd], M = fmaxf(m_run[jj], m1);
+          const float w0 = m_run[jj] == M ? 1.f : ex2_approx(m_run[jj] - M), w1 = m1 == M ? 1.f : ex2_approx(m1 - M);
+          o[jj] = o[jj] * w0 + x_o[hd * kD + t] * w1;
+          l[jj] = l[jj] * w0 + x_ml[16 + hd] * w1;
+          m_run[jj] = M;
+        }
+      }
+      named_bar(3, 32 * SW);
+      if (X == 1) continue;
       const float vs = FP8 ? a.kv.v_scale[g] : 1.f;
       uint16_t* out_row = a.out + a.pb.q_start[b] * a.ldo + (long long)g * G * kD + t;
       if (jb == 0 && je == w.nt) {
@@ -659,7 +724,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         }
       }
       __threadfence();
-      softmax_bar<32 * SW>();  // every thread's stores precede the count
+      named_bar(1, 32 * XW);  // every thread's stores precede the count
       if (threadIdx.x == 0) {
         int n = 0;
         for (int c = c_first; c <= c_last; ++c) n += cta_empty(c, U, n_cta) ? 0 : 1;
@@ -667,7 +732,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         __threadfence();
         *s_last = before == n - 1;
       }
-      softmax_bar<32 * SW>();
+      named_bar(1, 32 * XW);
       if (!*s_last) continue;
       // all partials are there: lane i weighs CTA c_first + i, 32 at a time
 #pragma unroll

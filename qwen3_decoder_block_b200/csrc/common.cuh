@@ -44,6 +44,15 @@ __device__ __forceinline__ void regs_increase() { asm volatile("setmaxnreg.inc.s
 template <int N>
 __device__ __forceinline__ void regs_decrease() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// One lane of a converged warp, chosen by the hardware: the compiler then knows that the code
+// under it runs in a single thread (tensor copies take uniform operands; under a plain lane
+// test they are issued from a loop over the lanes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
