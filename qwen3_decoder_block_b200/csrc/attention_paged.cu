@@ -23,6 +23,14 @@ constexpr float kScaleLog2 = 0.12751743074380304f;  // log2(e) / sqrt(128)
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte swizzle: 16 KB
 
+// Where a CTA's share of the work list starts (written by the plan kernel, so that a CTA finds
+// it with one load).
+struct __align__(32) CtaStart {
+  long long units;  // all units of the call
+  int b, g, j;      // sequence, KV group and tile of its first unit
+  int n_keys;       // keys of that row
+};
+
 struct PagedAttn {
   PagedBatch pb;
   KvPages kv;
@@ -32,6 +40,8 @@ struct PagedAttn {
   uint16_t* out;
   long long ldo;
   long long* plan;   // [B + 1] work-unit prefix of the sequences
+  CtaStart* start;   // [n_cta]
+  int n_cta;         // CTAs of the attention kernel
   int* counters;     // merge counters
   float* part;       // partial results
   uint8_t* q8;       // decode form, e4m3 pages: the queries' e4m3 terms [B][Hkv][2G][128]
@@ -116,6 +126,26 @@ __global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const P
     }
     if (threadIdx.x == 0) a.plan[B] = carry;
     for (int i = threadIdx.x; i < B * Hkv; i += kPlanThreads) a.counters[i] = 0;
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.n_cta; c += kPlanThreads) {
+      CtaStart s;
+      s.units = carry;
+      s.b = s.g = s.j = s.n_keys = 0;
+      const long long t = carry * c / a.n_cta;
+      if (t < carry * (c + 1) / a.n_cta) {
+        int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (a.plan[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        s.b = lo;
+        s.n_keys = a.pb.ctx_len[lo] + 1;
+        const int nt = (s.n_keys + kTileK - 1) / kTileK, at = (int)(t - a.plan[lo]);
+        s.g = at / nt;
+        s.j = at % nt;
+      }
+      a.start[c] = s;
+    }
     return;
   }
   const long long row = (long long)(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
@@ -171,51 +201,47 @@ struct DecodeCfg {
   static constexpr int kSetWarps = 4 * kHeadWarps;
   static constexpr int kSoftmaxWarps = 2 * kSetWarps;                 // set X takes the CTA's tiles of parity X
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
-  static constexpr int kStages = FP8 ? 5 : 3;
+  static constexpr int kStages = FP8 ? (G == 16 ? 5 : 6) : 3;
   static constexpr uint32_t kKV = FP8 ? kTile8 : 2 * kTile8;          // K or V of one tile
-  static constexpr uint32_t kQB = (FP8 ? 1 : 2) * kCols * 128;        // q rows of one tile
-  static constexpr uint32_t kStage = kKV + kQB;                       // K ring: a tile and its q rows; V ring: kKV
-  static constexpr uint32_t kOffV = kStages * kStage;
+  static constexpr uint32_t kQB = (FP8 ? 1 : 2) * kCols * 128;        // q of one row
+  static constexpr uint32_t kOffV = kStages * kKV;                    // K ring, V ring, q of two rows
+  static constexpr uint32_t kOffQ = 2 * kStages * kKV;
   static constexpr uint32_t kPB = (FP8 ? 1 : 2) * kCols * 128;        // one P buffer
-  static constexpr uint32_t kOffP = kOffV + kStages * kKV;
+  static constexpr uint32_t kOffP = kOffQ + 2 * kQB;
   static constexpr uint32_t kOffRed = kOffP + 2 * kPB;                // per set: maxima [2][4][16], sums [4][16]
   static constexpr uint32_t kOffX = kOffRed + 2 * 3 * 64 * 4;         // set 1's row: o [G][128], m [16], l [16]
   static constexpr uint32_t kOffBar = kOffX + G * kD * 4 + 2 * 16 * 4;
-  static constexpr uint32_t kSmem = kOffBar + (4 * kStages + 10) * 8 + 16 + 1024;
+  static constexpr uint32_t kSmem = kOffBar + (4 * kStages + 14) * 8 + 16 + 1024;
   // tensor memory: S of set 0 and 1, O of set 0 and 1
   static constexpr uint32_t kTmem = 4 * kCols <= 64 ? 64 : (4 * kCols <= 128 ? 128 : 256);
 };
 
-// Walk over the (sequence, group) rows that meet this CTA's tiles.
+// Walk over the (sequence, group) rows that meet this CTA's tiles: tiles [j0, j1) of the row.
 struct RowWalk {
   const long long* plan;
   const int* ctx_len;
-  int B, Hkv, b, g, nt, n_keys;
-  long long rs, t_begin, t_end;  // rs: index of the current row's first tile
-  __device__ RowWalk(const PagedAttn& a, int b0, long long tb, long long te)
-      : plan(a.plan), ctx_len(a.pb.ctx_len), B(a.pb.B), Hkv(a.kv.Hkv), b(b0), g(0), nt(0), n_keys(0), rs(te),
-        t_begin(tb), t_end(te) {
-    if (tb < te) {
-      set_seq();
-      g = (int)((tb - plan[b]) / nt);
-      rs = plan[b] + (long long)g * nt;
-    }
+  int B, Hkv, b, g, j0, j1, nt, n_keys;
+  int left;  // the CTA's tiles from the current row on
+  __device__ RowWalk(const PagedAttn& a, const CtaStart& s, int n_tiles)
+      : plan(a.plan), ctx_len(a.pb.ctx_len), B(a.pb.B), Hkv(a.kv.Hkv), b(s.b), g(s.g), j0(s.j), n_keys(s.n_keys),
+        left(n_tiles) {
+    set_row();
   }
-  __device__ void set_seq() {
-    n_keys = ctx_len[b] + 1;
+  __device__ void set_row() {
     nt = (n_keys + kTileK - 1) / kTileK;
+    j1 = min(nt, j0 + left);
   }
-  __device__ bool valid() const { return rs < t_end; }
-  __device__ int j0() const { return (int)((t_begin > rs ? t_begin : rs) - rs); }
-  __device__ int j1() const { return (int)((t_end < rs + nt ? t_end : rs + nt) - rs); }
+  __device__ bool valid() const { return left > 0; }
   __device__ void next() {
-    rs += nt;
+    left -= j1 - j0;
+    if (left <= 0) return;
+    j0 = 0;
     if (++g == Hkv) {
       g = 0;
       do { ++b; } while (b < B && plan[b + 1] == plan[b]);
-      if (b < B && rs < t_end) set_seq();
-      else rs = t_end;
+      n_keys = ctx_len[b < B ? b : B - 1] + 1;
     }
+    set_row();
   }
 };
 
@@ -294,35 +320,31 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   uint64_t* k_empty = k_full + NS;                                    // [NS] ... consumed
   uint64_t* v_full = k_full + 2 * NS;                                 // [NS] V loaded
   uint64_t* v_empty = k_full + 3 * NS;                                // [NS] ... consumed
-  uint64_t* s_full = k_full + 4 * NS;  // [2] scores of set X ready
+  uint64_t* q_full = k_full + 4 * NS;  // [2] q of a row loaded
+  uint64_t* q_empty = q_full + 2;      // [2] ... consumed
+  uint64_t* s_full = q_full + 4;       // [2] scores of set X ready
   uint64_t* s_empty = s_full + 2;  // [2] scores of set X read
   uint64_t* p_full = s_full + 4;   // [2] P of set X written (and its O rescaled)
   uint64_t* pv_done = s_full + 6;  // [2] P.V of set X's tile complete
   uint64_t* drain = s_full + 8;    // [2] an issuer's MMAs complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 10);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_b0 = s_abort + 1;    // sequence holding this CTA's first tile
-  volatile int* s_last = s_abort + 2;  // this CTA merges the row
+  volatile int* s_last = s_abort + 1;  // this CTA merges the row
   int* err = a.err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * NS; ++i) mbar_init(&k_full[i], 1);
+    for (int i = 0; i < 4 * NS + 4; ++i) mbar_init(&k_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], XW);
       mbar_init(&p_full[i], XW); mbar_init(&pv_done[i], 1); mbar_init(&drain[i], 1);
     }
     *s_abort = 0;
-    *s_b0 = 0;
     fence_barrier_init();
   }
   // Unused rows of the Q and P operand tiles are never written: clear all of them once.
-  for (int i = threadIdx.x; i < (int)((NS * C::kQB + 2 * C::kPB) / 16); i += blockDim.x) {
-    const uint32_t off = 16u * i;
-    uint8_t* p = off < NS * C::kQB ? smem + (off / C::kQB) * C::kStage + C::kKV + off % C::kQB
-                                   : smem + C::kOffP + (off - NS * C::kQB);
-    *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-  }
+  for (int i = threadIdx.x; i < (int)((2 * C::kQB + 2 * C::kPB) / 16); i += blockDim.x)
+    reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (threadIdx.x == 32 * SW) {
     tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV);
@@ -336,128 +358,136 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   const uint32_t tmO = tmem + 2 * NC;
   pdl_wait();
   pdl_trigger();
-  const int B = a.pb.B, Hkv = a.kv.Hkv;
-  const long long U = a.plan[B];
-  const int n_cta = (int)gridDim.x;
-  const long long t_begin = U * blockIdx.x / n_cta, t_end = U * (blockIdx.x + 1) / n_cta;
-  for (int b = threadIdx.x; b < B; b += blockDim.x)
-    if (a.plan[b] <= t_begin && t_begin < a.plan[b + 1]) *s_b0 = b;
-  __syncthreads();
-  const int b0 = *s_b0;
+  const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
+  const CtaStart start = a.start[blockIdx.x];
+  const long long U = start.units;
+  const int n_tiles = (int)(U * (blockIdx.x + 1) / n_cta - U * blockIdx.x / n_cta);
 
   if (warp == SW || warp == SW + 3) {
     // -------------------------------------------------- TMA producers: K and q; V
     // One box per page of a tile, min(page, 128) keys each (16 in a row's last tile, so that
     // nothing past its last 16 keys is read), twice for the two 64-dim halves of bf16. Lane i
-    // looks up the page of box i, a tile ahead: the load lands while the ring is full.
+    // finds box i's page, a tile ahead, and its cache row; the rows go round by shuffles and
+    // one elected lane issues the copies (about 30 clocks each; found by that lane alone, or
+    // issued from a lane loop, a box costs about 180 or 95).
     const bool is_v = warp == SW + 3;
     const CUtensorMap* map = is_v ? &tmV : &tmK;
     const CUtensorMap* map16 = is_v ? &tmV16 : &tmK16;
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
-    const uint32_t ring = is_v ? C::kOffV : 0, stage = is_v ? C::kKV : C::kStage;
-    const int shift = a.kv.page_shift, box_shift = min(shift, 7);
-    const int rows_all = (int)(((long long)a.kv.n_pages * Hkv) << shift);
-    RowWalk w(a, b0, t_begin, t_end);
-    int j = w.valid() ? w.j0() : 0, je = w.valid() ? w.j1() : 0;
-    // the page of this lane's box in tile j of row w
-    auto lane_page = [&]() {
+    uint8_t* ring = smem + (is_v ? C::kOffV : 0);
+    const int shift = a.kv.page_shift, in_page = (1 << shift) - 1, box_shift = min(shift, 7);
+    const int n_pages = a.kv.n_pages, rows_all = (n_pages * Hkv) << shift;
+    RowWalk w(a, start, n_tiles);
+    int j = w.j0;
+    // the page of this lane's box in tile j of row w (0 where it has none)
+    auto look_up = [&]() {
       const int left = w.n_keys - j * kTileK;
-      const int bs = left >= kTileK ? box_shift : 4;
-      const int key = j * kTileK + (lane << bs);
-      if (lane >= (kTileK >> bs) || key >= w.n_keys) return -1;
-      return __ldg(a.pb.table + (long long)w.b * a.pb.max_pages + (key >> shift));
+      const int off = lane << (left >= kTileK ? box_shift : 4);
+      if (off >= kTileK || off >= left) return 0;
+      return __ldg(a.pb.table + (long long)w.b * a.pb.max_pages + ((j * kTileK + off) >> shift));
     };
-    int page = w.valid() ? lane_page() : -1;
-    int st = 0, n_tiles = 0;
+    int page = w.valid() ? look_up() : 0;
+    int st = 0, done = 0, rows_seen = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, new_row = true;
     while (w.valid()) {
       const int b = w.b, g = w.g, k0 = j * kTileK, left = w.n_keys - k0;
-      const int cur_page = page;
-      if (++j >= je) {
-        w.next();
-        if (w.valid()) {
-          j = w.j0();
-          je = w.j1();
-        }
-      }
-      if (w.valid()) page = lane_page();
-      ok = !*s_abort && mbar_wait(&empty[st], phase ^ 1u, err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      uint8_t* base = smem + ring + st * stage;
       const bool tail = left < kTileK;
       const int bs = tail ? 4 : box_shift;
       const int n = tail ? (left + 15) >> 4 : kTileK >> bs;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&full[st], (n << bs) * 128 * (FP8 ? 1 : 2) +
-                                             (is_v ? 0 : C::kQTerms * G * 128 * (FP8 ? 1 : 2)));
-        if (!is_v) {
+      // a bad page reads as zeros: behind the tensor map's last row
+      const bool in = (unsigned)page < (unsigned)n_pages;
+      if (!in) record_error(err, kErrInvalid);
+      const int my_row = in ? ((page * Hkv + g) << shift) + ((k0 + (lane << bs)) & in_page) : rows_all;
+      int row[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, my_row, i);
+      if (!is_v && new_row) {
+        const int qs = rows_seen & 1;
+        ok = !*s_abort && mbar_wait(&q_empty[qs], (uint32_t)((rows_seen >> 1) & 1) ^ 1u, err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const int tok = FP8 ? 0 : a.pb.q_start[b];
+        uint8_t* dst = smem + C::kOffQ + qs * C::kQB;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&q_full[qs], C::kQTerms * G * 128 * (FP8 ? 1 : 2));
           if (FP8) {
-            tma_load_2d(base + C::kKV, &tmQ, &full[st], 0, (b * Hkv + g) * 2 * G);
+            tma_load_2d(dst, &tmQ, &q_full[qs], 0, (b * Hkv + g) * 2 * G);
           } else {
-            const int tok = a.pb.q_start[b];
-            tma_load_3d(base + C::kKV, &tmQ, &full[st], 0, g * G, tok);
-            tma_load_3d(base + C::kKV + NC * 128, &tmQ, &full[st], 64, g * G, tok);
+            tma_load_3d(dst, &tmQ, &q_full[qs], 0, g * G, tok);
+            tma_load_3d(dst + NC * 128, &tmQ, &q_full[qs], 64, g * G, tok);
           }
         }
+        __syncwarp();
+        ++rows_seen;
+      }
+      new_row = ++j == w.j1;
+      if (new_row) {
+        w.next();
+        j = w.j0;
+      }
+      if (w.valid()) page = look_up();
+      ok = !*s_abort && mbar_wait(&empty[st], phase ^ 1u, err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      uint8_t* dst = ring + st * C::kKV;
+      if (elect_one()) {
+        const CUtensorMap* m = tail ? map16 : map;
+        mbar_arrive_expect_tx(&full[st], (n << bs) * 128 * (FP8 ? 1 : 2));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < n) {
+            tma_load_2d(dst + ((i << bs) * 128), m, &full[st], 0, row[i]);
+            if (!FP8) tma_load_2d(dst + kTile8 + ((i << bs) * 128), m, &full[st], 64, row[i]);
+          }
       }
       __syncwarp();
-      if (lane < n && (cur_page < 0 || cur_page >= a.kv.n_pages)) record_error(err, kErrInvalid);
-      const CUtensorMap* m = tail ? map16 : map;
-      for (int i = 0; i < n; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, cur_page, i);
-        // a bad page reads as zeros: behind the tensor map's last row
-        const int row = pg < 0 || pg >= a.kv.n_pages
-                            ? rows_all
-                            : ((pg * Hkv + g) << shift) + ((k0 + (i << bs)) & ((1 << shift) - 1));
-        uint8_t* dst = base + ((i << bs) * 128);
-        if (elect_one()) {
-          tma_load_2d(dst, m, &full[st], 0, row);
-          if (!FP8) tma_load_2d(dst + kTile8, m, &full[st], 64, row);
-        }
-        __syncwarp();
-      }
-      ++n_tiles;
+      ++done;
       if (++st == NS) { st = 0; phase ^= 1u; }
     }
     if (!ok) {
       *s_abort = 1;
       // let the copies still in flight land before the CTA exits
-      for (int i = n_tiles > NS ? n_tiles - NS : 0; i < n_tiles; ++i)
-        mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), err);
+      for (int i = done > NS ? done - NS : 0; i < done; ++i) mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), err);
+      if (!is_v)
+        for (int i = rows_seen > 2 ? rows_seen - 2 : 0; i < rows_seen; ++i)
+          mbar_wait(&q_full[i & 1], (uint32_t)((i >> 1) & 1), err);
     }
   } else if (warp == SW + 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ S issuer: S = K q
       constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 0, 0) : idesc_bf16_f32(128, NC, 0, 0);
-      const int n_tiles = (int)(t_end - t_begin);
-      int st = 0;
+      int tc = 0, st = 0, rows_seen = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tc = 0; tc < n_tiles && ok; ++tc) {
-        const int sb = tc & 1;
-        if (*s_abort || !mbar_wait(&k_full[st], phase, err)) { ok = false; break; }
-        if (tc >= 2 && (*s_abort || !mbar_wait(&s_empty[sb], (uint32_t)(((tc - 2) >> 1) & 1), err))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sK = smem_u32(smem + st * C::kStage), sQ = sK + C::kKV;
-        if (FP8) {
+      for (RowWalk w(a, start, n_tiles); w.valid() && ok; w.next(), ++rows_seen) {
+        const int qs = rows_seen & 1;
+        if (*s_abort || !mbar_wait(&q_full[qs], (uint32_t)((rows_seen >> 1) & 1), err)) { ok = false; break; }
+        const uint32_t sQ = smem_u32(smem + C::kOffQ + qs * C::kQB);
+        for (int j = w.j0; j < w.j1; ++j, ++tc) {
+          const int sb = tc & 1;
+          if (*s_abort || !mbar_wait(&k_full[st], phase, err)) { ok = false; break; }
+          if (tc >= 2 && (*s_abort || !mbar_wait(&s_empty[sb], (uint32_t)(((tc - 2) >> 1) & 1), err))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sK = smem_u32(smem + st * C::kKV);
+          if (FP8) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_e4m3_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK) + 2 * kk, sdesc_kmajor_sw128(sQ) + 2 * kk, idesc,
-                        kk ? 1u : 0u);
-        } else {
+            for (int kk = 0; kk < 4; ++kk)
+              mma_e4m3_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK) + 2 * kk, sdesc_kmajor_sw128(sQ) + 2 * kk, idesc,
+                          kk ? 1u : 0u);
+          } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK + (kk >> 2) * kTile8) + 2 * (kk & 3),
-                        sdesc_kmajor_sw128(sQ + (kk >> 2) * NC * 128) + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK + (kk >> 2) * kTile8) + 2 * (kk & 3),
+                          sdesc_kmajor_sw128(sQ + (kk >> 2) * NC * 128) + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+          }
+          mma_commit(&s_full[sb]);
+          mma_commit(&k_empty[st]);
+          if (++st == NS) { st = 0; phase ^= 1u; }
         }
-        mma_commit(&s_full[sb]);
-        mma_commit(&k_empty[st]);
-        if (++st == NS) { st = 0; phase ^= 1u; }
+        if (ok) mma_commit(&q_empty[qs]);
       }
       if (!ok) *s_abort = 1;
       mma_commit(&drain[0]);  // every MMA completes before the tensor memory is released
@@ -470,8 +500,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       int tc = 0, st = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (RowWalk w(a, b0, t_begin, t_end); w.valid() && ok; w.next()) {
-        const int jb = w.j0(), je = w.j1();
+      for (RowWalk w(a, start, n_tiles); w.valid() && ok; w.next()) {
+        const int jb = w.j0, je = w.j1;
         for (int j = jb; j < je; ++j, ++tc) {
           const int pb = tc & 1;
           if (*s_abort || !mbar_wait(&v_full[st], phase, err) ||
@@ -524,9 +554,9 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     int tc0 = 0;  // the CTA's tiles before the current row
     int u = 0;    // the set's tiles so far
     bool ok = true;
-    for (RowWalk w(a, b0, t_begin, t_end); w.valid(); w.next()) {
+    for (RowWalk w(a, start, n_tiles); w.valid(); w.next()) {
       const int b = w.b, g = w.g, bg = b * Hkv + g;
-      const int jb = w.j0(), je = w.j1();
+      const int jb = w.j0, je = w.j1;
       float factor[GH], m_run[GH], l_part[GH];
 #pragma unroll
       for (int jj = 0; jj < GH; ++jj) {
@@ -708,7 +738,9 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       }
       // a row shared by several CTAs: partial to slot row + CTA (unique: rows and CTA ranges
       // are both in tile order), then count it
-      const int c_first = cta_of(w.rs, U, n_cta), c_last = cta_of(w.rs + w.nt - 1, U, n_cta);
+      const long long rs = a.plan[b] + (long long)g * w.nt;
+      const int c_first = cta_of(rs, U, n_cta), c_last = cta_of(rs + w.nt - 1, U, n_cta);
+      const bool sparse = U < n_cta;  // one tile a CTA, some CTAs without any
       float* row_part = a.part + (long long)bg * G * kPartFloats;
       const long long stride = (long long)G * kPartFloats;
       {
@@ -723,14 +755,10 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           }
         }
       }
-      __threadfence();
       named_bar(1, 32 * XW);  // every thread's stores precede the count
       if (threadIdx.x == 0) {
-        int n = 0;
-        for (int c = c_first; c <= c_last; ++c) n += cta_empty(c, U, n_cta) ? 0 : 1;
-        const int before = ok ? atomicAdd(&a.counters[bg], 1) : -1;
-        __threadfence();
-        *s_last = before == n - 1;
+        const int n = sparse ? w.nt : c_last - c_first + 1;
+        *s_last = ok && atom_add_acq_rel_gpu(&a.counters[bg], 1) == n - 1;
       }
       named_bar(1, 32 * XW);
       if (!*s_last) continue;
@@ -740,13 +768,13 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         const float* hp = row_part + (j0 + jj) * kPartFloats;
         float M = -INFINITY;
         for (int c = c_first + lane; c <= c_last; c += 32)
-          if (!cta_empty(c, U, n_cta)) M = fmaxf(M, __ldcg(hp + c * stride + kD));
+          if (!sparse || !cta_empty(c, U, n_cta)) M = fmaxf(M, __ldcg(hp + c * stride + kD));
         M = warp_max(M);
         float L = 0.f, acc = 0.f;
         for (int base = c_first; base <= c_last; base += 32) {
           const int c = base + lane;
           float wgt = 0.f;
-          if (c <= c_last && !cta_empty(c, U, n_cta)) {
+          if (c <= c_last && !(sparse && cta_empty(c, U, n_cta))) {
             wgt = exp2f(__ldcg(hp + c * stride + kD) - M);
             L += __ldcg(hp + c * stride + kD + 1) * wgt;
           }
@@ -872,15 +900,16 @@ __global__ void __launch_bounds__(128) attn_paged_simple_kernel(const PagedBatch
 // ----------------------------------------------------------------------------
 namespace {
 
-// Scratch of a call, in order: work list, merge counters, partials, e4m3 query terms and scales.
+// Scratch of a call, in order: work list, CTA starts, merge counters, partials, e4m3 query terms and scales.
 struct Scratch {
-  size_t plan, counters, part, q8, q8_scale, bytes;
+  size_t plan, start, counters, part, q8, q8_scale, bytes;
 };
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 Scratch scratch_of(int B, int Hq, int Hkv, int max_q) {
   Scratch s;
   s.plan = 0;
-  s.counters = s.plan + up256(((size_t)B + 1) * sizeof(long long));
+  s.start = s.plan + up256(((size_t)B + 1) * sizeof(long long));
+  s.counters = s.start + kMaxCtas * sizeof(CtaStart);
   const bool decode = max_q == 1;
   const int G = Hq / Hkv;
   s.part = s.counters + up256(decode ? (size_t)B * Hkv * sizeof(int) : 256);
@@ -911,8 +940,7 @@ int launch_decode(const PagedAttn& a, const CUtensorMap& tmQ, cudaStream_t s) {
   if (page_maps(a.kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
   auto kernel = attn_paged_decode_kernel<G, FP8>;
   if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem)) return -6;
-  const int grid = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
-  q3_launch(kernel, grid, C::kThreads, C::kSmem, s, tmQ, tmK, tmV, tmK16, tmV16, a);
+  q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmQ, tmK, tmV, tmK16, tmV16, a);
   return 0;
 }
 
@@ -958,6 +986,8 @@ int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int m
   a.q = q; a.ldq = ldq;
   a.out = out; a.ldo = ldo;
   a.plan = reinterpret_cast<long long*>(base + off.plan);
+  a.start = reinterpret_cast<CtaStart*>(base + off.start);
+  a.n_cta = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
   a.counters = reinterpret_cast<int*>(base + off.counters);
   a.part = reinterpret_cast<float*>(base + off.part);
   a.q8 = base + off.q8;

@@ -120,11 +120,6 @@ __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ int atom_add_acq_rel_gpu(int* p, int v) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
 __device__ __forceinline__ bool grid_barrier(int* bar, int n, int* err) {
   const int g0 = ld_acquire_gpu(bar + 1);  // cannot advance before this CTA arrives
   if (atom_add_acq_rel_gpu(bar, 1) == n - 1) {
