@@ -76,7 +76,13 @@ __device__ __forceinline__ int cta_of(long long t, long long U, int n) { return 
 // Whether CTA c's range is empty (only when U < n).
 __device__ __forceinline__ bool cta_empty(int c, long long U, int n) { return U * c / n == U * (c + 1) / n; }
 
+// First unit of CTA c's range.
+__device__ __forceinline__ long long share(long long U, int c, int n) {
+  return U < (1 << 22) ? (long long)((unsigned)U * (unsigned)c / (unsigned)n) : U * c / n;  // c, n <= 256
+}
+
 constexpr int kPlanThreads = 256;
+constexpr int kPlanShared = 1024;  // sequences whose prefix is also kept in shared memory
 
 // Exclusive prefix sums of v over the block, in order of the threads; *total: the block's sum.
 __device__ __forceinline__ long long block_prefix(long long v, long long* wsum, long long* total) {
@@ -113,6 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const P
   const int B = a.pb.B, Hkv = a.kv.Hkv;
   if (blockIdx.x == 0) {
     __shared__ long long wsum[kPlanThreads / 32];
+    __shared__ long long plan_s[kPlanShared];
     long long carry = 0;
     for (int base = 0; base < B; base += kPlanThreads) {
       const int b = base + (int)threadIdx.x;
@@ -122,8 +129,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const P
         v = (long long)Hkv * ((ctx + kTileK) / kTileK);
       const long long at = block_prefix(v, wsum, &total);
       if (b < B) a.plan[b] = carry + at;
+      if (b < kPlanShared) plan_s[b] = carry + at;
       carry += total;
     }
+    const long long* plan = B <= kPlanShared ? plan_s : a.plan;
     if (threadIdx.x == 0) a.plan[B] = carry;
     for (int i = threadIdx.x; i < B * Hkv; i += kPlanThreads) a.counters[i] = 0;
     __syncthreads();
@@ -131,16 +140,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const P
       CtaStart s;
       s.units = carry;
       s.b = s.g = s.j = s.n_keys = 0;
-      const long long t = carry * c / a.n_cta;
-      if (t < carry * (c + 1) / a.n_cta) {
+      const long long t = share(carry, c, a.n_cta);
+      if (t < share(carry, c + 1, a.n_cta)) {
         int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (a.plan[mid] <= t) lo = mid; else hi = mid - 1;
+          if (plan[mid] <= t) lo = mid; else hi = mid - 1;
         }
         s.b = lo;
         s.n_keys = a.pb.ctx_len[lo] + 1;
-        const int nt = (s.n_keys + kTileK - 1) / kTileK, at = (int)(t - a.plan[lo]);
+        const int nt = (s.n_keys + kTileK - 1) / kTileK, at = (int)(t - plan[lo]);
         s.g = at / nt;
         s.j = at % nt;
       }
@@ -361,7 +370,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
   const CtaStart start = a.start[blockIdx.x];
   const long long U = start.units;
-  const int n_tiles = (int)(U * (blockIdx.x + 1) / n_cta - U * blockIdx.x / n_cta);
+  const int n_tiles = (int)(share(U, blockIdx.x + 1, n_cta) - share(U, blockIdx.x, n_cta));
 
   if (warp == SW || warp == SW + 3) {
     // -------------------------------------------------- TMA producers: K and q; V
@@ -762,32 +771,60 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       }
       named_bar(1, 32 * XW);
       if (!*s_last) continue;
-      // all partials are there: lane i weighs CTA c_first + i, 32 at a time
+      // all partials are there: lane i weighs CTA c_first + i, 32 at a time, then the thread
+      // sums its dim of them, kBatch loads in flight (one at a time they cost 8 us a row)
+      constexpr int kBatch = 32 / GH;
+      const float* part = row_part + j0 * kPartFloats;
+      auto piece = [&](int c) { return c <= c_last && !(sparse && cta_empty(c, U, n_cta)); };
+      float M[GH], m0[GH], l0[GH], L[GH], acc[GH];
 #pragma unroll
       for (int jj = 0; jj < GH; ++jj) {
-        const float* hp = row_part + (j0 + jj) * kPartFloats;
-        float M = -INFINITY;
-        for (int c = c_first + lane; c <= c_last; c += 32)
-          if (!sparse || !cta_empty(c, U, n_cta)) M = fmaxf(M, __ldcg(hp + c * stride + kD));
-        M = warp_max(M);
-        float L = 0.f, acc = 0.f;
-        for (int base = c_first; base <= c_last; base += 32) {
-          const int c = base + lane;
-          float wgt = 0.f;
-          if (c <= c_last && !(sparse && cta_empty(c, U, n_cta))) {
-            wgt = exp2f(__ldcg(hp + c * stride + kD) - M);
-            L += __ldcg(hp + c * stride + kD + 1) * wgt;
-          }
-          const int n = min(32, c_last - base + 1);
-#pragma unroll 8
-          for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wgt, i);
-            if (wi != 0.f) acc += __ldcg(hp + (base + i) * stride + t) * wi;
-          }
+        m0[jj] = -INFINITY;
+        l0[jj] = L[jj] = acc[jj] = 0.f;
+        if (piece(c_first + lane)) {
+          m0[jj] = __ldcg(part + (c_first + lane) * stride + jj * kPartFloats + kD);
+          l0[jj] = __ldcg(part + (c_first + lane) * stride + jj * kPartFloats + kD + 1);
         }
-        L = warp_sum(L);
-        out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, acc * vs / L);
+        M[jj] = m0[jj];
       }
+      for (int c = c_first + 32 + lane; c <= c_last; c += 32)
+        if (piece(c))
+#pragma unroll
+          for (int jj = 0; jj < GH; ++jj) M[jj] = fmaxf(M[jj], __ldcg(part + c * stride + jj * kPartFloats + kD));
+#pragma unroll
+      for (int jj = 0; jj < GH; ++jj) M[jj] = warp_max(M[jj]);
+      for (int base = c_first; base <= c_last; base += 32) {
+        const int c = base + lane;
+        float wgt[GH];
+#pragma unroll
+        for (int jj = 0; jj < GH; ++jj) {
+          if (base != c_first) {
+            m0[jj] = piece(c) ? __ldcg(part + c * stride + jj * kPartFloats + kD) : -INFINITY;
+            l0[jj] = piece(c) ? __ldcg(part + c * stride + jj * kPartFloats + kD + 1) : 0.f;
+          }
+          wgt[jj] = piece(c) ? exp2f(m0[jj] - M[jj]) : 0.f;
+          L[jj] += l0[jj] * wgt[jj];
+        }
+        const int n = min(32, c_last - base + 1);
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+          float v[kBatch][GH];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int jj = 0; jj < GH; ++jj)
+              v[i][jj] = i0 + i < n ? __ldcg(part + (base + i0 + i) * stride + jj * kPartFloats + t) : 0.f;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int jj = 0; jj < GH; ++jj) {
+              const float wi = __shfl_sync(0xffffffffu, wgt[jj], (i0 + i) & 31);
+              acc[jj] += wi != 0.f ? v[i][jj] * wi : 0.f;  // the slot of an empty CTA holds anything
+            }
+        }
+      }
+#pragma unroll
+      for (int jj = 0; jj < GH; ++jj)
+        out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, acc[jj] * vs / warp_sum(L[jj]));
     }
     if (!ok) *s_abort = 1;
   }
