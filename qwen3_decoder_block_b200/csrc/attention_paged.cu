@@ -31,6 +31,8 @@ struct __align__(32) CtaStart {
   int n_keys;       // keys of that row
 };
 
+struct ChunkMeta;
+
 struct PagedAttn {
   PagedBatch pb;
   KvPages kv;
@@ -42,7 +44,8 @@ struct PagedAttn {
   long long* plan;   // [B + 1] work-unit prefix of the sequences
   CtaStart* start;   // [n_cta]
   int n_cta;         // CTAs of the attention kernel
-  int* counters;     // merge counters
+  int* counters;     // decode form: merge counters [B * Hkv]
+  ChunkMeta* meta;   // chunk form: [n_cta][2]
   float* part;       // partial results
   uint8_t* q8;       // decode form, e4m3 pages: the queries' e4m3 terms [B][Hkv][2G][128]
   float* q8_scale;   // [B][Hq]
@@ -837,99 +840,781 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   }
 }
 
-// One warp per (token, query head): 32 keys at a time, a lane's dot product per key, online
-// softmax over the warp, then 4 output dims per lane.
-template <bool FP8>
-__global__ void __launch_bounds__(128) attn_paged_simple_kernel(const PagedBatch pb, const KvPages kv, int Hq,
-                                                                int n_tokens, int max_q, const uint16_t* q,
-                                                                long long ldq, uint16_t* out, long long ldo,
-                                                                int o_f16, int* err) {
-  __shared__ float qs[4][128];
+// ============================================================================
+// Chunk form: any number of new tokens a sequence, decode tokens among them. The 128-row MMA
+// tile packs TQ = 128 / G tokens x the G query heads of one KV group, so every K/V tile is
+// loaded once for the group; one softmax warpgroup X (one row a thread) per S_X, P_X, O_X in
+// tensor memory, two of them a CTA. An item of work is
+//   pair:   two Q tiles of a sequence and KV group; warpgroup X takes Q tile X through every
+//           KV tile, both Q tiles sharing the tile's loads;
+//   single: the last Q tile of an odd count (all a decode token or a short chunk has);
+//           warpgroup X takes every second KV tile, and warpgroup 0 joins the halves at the
+//           end, reading O_1 from tensor memory (the lanes are the same).
+// Work units are KV tiles (two for a pair's tile); each CTA gets the same share of the units,
+// so a long context is split over the SMs as far as the batch leaves them idle, and few Q
+// tiles cost no idle SM. An item that spans CTAs leaves partials (at most four a CTA), joined
+// by a kernel that follows.
+//
+// e4m3 pages: S takes K as it is (kind::f8f6f4) against q split into two e4m3 terms of one
+// scale (exact for bf16 values down to 2^-10 of the row's largest; below, off by at most 2^-18
+// of it). For P.V a third warpgroup widens V to fp16 in shared memory, which is exact, and P is
+// fp16 scaled to at most 2^15: 2^-11 of each weight, or 2^-31 of the row's largest, is finer
+// than bf16, and one cvt widens two values.
+// ============================================================================
+namespace {
+
+constexpr int kChunkCtas = 152;                       // grid bound (partials are sized by it)
+constexpr int kChunkPart = kD * 128 + 2 * 128;        // o [128 dims][128 rows], m [128], l [128]
+
+struct ChunkMeta {
+  int split;   // the CTA's last item of warpgroup X goes on in other CTAs
+  int c_last;  // the last of them
+  int n_rows;  // valid rows of the Q tile
+  int tok;     // first token row
+  int g;
+  int has;     // the CTA left a partial of an item that an earlier CTA began
+  int pad[2];
+};
+
+// Sum over p < P of the KV tiles of pair p, floor((ctx + min((p + 1) s, n_q) - 1) / 128) + 1, for
+// s = 2 TQ (a power of two, 16 to 256) and P <= ceil(n_q / s).
+__device__ __forceinline__ long long pair_tiles(int ctx, int n_q, int s, int P) {
+  if (P <= 0) return 0;
+  long long cut = 0;
+  if ((long long)P * s > n_q) {  // the last pair ends with the sequence
+    cut = ((long long)ctx + n_q - 1) / kTileK + 1;
+    --P;
+  }
+  const long long a = (long long)ctx + s - 1;
+  if (s >= kTileK) return cut + P * (a / kTileK + 1) + (long long)(s / kTileK) * P * (P - 1) / 2;
+  const int r = kTileK / s;  // floor((a + p s) / 128) = floor((floor(a / s) + p) / r)
+  auto F = [&](long long n) {
+    const long long m = n / r;
+    return r * (m * (m - 1) / 2) + m * (n - m * r);
+  };
+  return cut + P + F(a / s + P) - F(a / s);
+}
+struct ChunkSeq {
+  int n_q, ctx, s, pairs, odd;
+  long long head_units;  // of one KV head
+  __device__ ChunkSeq(int nq, int c, int G) : n_q(nq), ctx(c), s(256 / G) {
+    const int tiles = (int)(((long long)nq * G + 127) / 128);
+    pairs = tiles >> 1;
+    odd = tiles & 1;
+    head_units = 2 * pair_tiles(ctx, n_q, s, pairs) + (odd ? ((long long)ctx + n_q - 1) / kTileK + 1 : 0);
+  }
+};
+
+}  // namespace
+
+// Chunk form, before the attention: the work list and the CTA starts.
+__global__ void __launch_bounds__(kPlanThreads) paged_chunk_plan_kernel(const PagedAttn a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long item = (long long)blockIdx.x * 4 + w;
-  const int tok = (int)(item / Hq), h = (int)(item % Hq);
-  if (tok >= n_tokens) return;
-  const int b = paged_seq_of(pb, tok, lane);
-  if (b >= pb.B) return;
-  const int start = pb.q_start[b], t = tok - start, n_q = pb.q_start[b + 1] - start, ctx = pb.ctx_len[b];
-  if (t < 0 || ctx < 0 || n_q > max_q || start < 0) {
-    if (lane == 0) record_error(err, kErrInvalid);
-    return;
+  __shared__ long long wsum[kPlanThreads / 32];
+  __shared__ long long plan_s[kPlanShared];
+  const int B = a.pb.B, Hkv = a.kv.Hkv, G = a.Hq / Hkv;
+  long long carry = 0;
+  for (int base = 0; base < B; base += kPlanThreads) {
+    const int b = base + (int)threadIdx.x;
+    long long v = 0, total;
+    int n_q, ctx;
+    if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err) && n_q > 0) v = Hkv * ChunkSeq(n_q, ctx, G).head_units;
+    const long long at = block_prefix(v, wsum, &total);
+    if (b < B) a.plan[b] = carry + at;
+    if (b < kPlanShared) plan_s[b] = carry + at;
+    carry += total;
   }
-  if (((long long)ctx + n_q - 1) >> kv.page_shift >= pb.max_pages) {
-    if (lane == 0) record_error(err, kErrCapacity);
-    return;
+  const long long* plan = B <= kPlanShared ? plan_s : a.plan;
+  if (threadIdx.x == 0) a.plan[B] = carry;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.n_cta; c += kPlanThreads) {
+    CtaStart s;
+    s.units = carry;
+    s.b = s.g = s.j = 0;
+    s.n_keys = 0;
+    const long long t = share(carry, c, a.n_cta);
+    if (t < share(carry, c + 1, a.n_cta)) {
+      int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (plan[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      s.b = lo;
+      const ChunkSeq q(a.pb.q_start[lo + 1] - a.pb.q_start[lo], a.pb.ctx_len[lo], G);
+      long long r = t - plan[lo];
+      s.g = (int)(r / q.head_units);
+      r -= s.g * q.head_units;
+      lo = 0;
+      hi = q.pairs;  // the last item that starts at or before unit r of the head
+      if (!q.odd) --hi;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (2 * pair_tiles(q.ctx, q.n_q, q.s, mid) <= r) lo = mid; else hi = mid - 1;
+      }
+      s.j = lo;
+      s.n_keys = (int)(r - 2 * pair_tiles(q.ctx, q.n_q, q.s, lo));  // units of the item before the CTA's
+    }
+    a.start[c] = s;
   }
-  const int g = h / (Hq / kv.Hkv);
-  const float ks = FP8 ? kv.k_scale[g] : 1.f, vs = FP8 ? kv.v_scale[g] : 1.f;
-  const uint2 qv = *reinterpret_cast<const uint2*>(q + tok * ldq + (long long)h * 128 + 4 * lane);
-  qs[w][4 * lane] = bf16_lo(qv.x);
-  qs[w][4 * lane + 1] = bf16_hi(qv.x);
-  qs[w][4 * lane + 2] = bf16_lo(qv.y);
-  qs[w][4 * lane + 3] = bf16_hi(qv.y);
-  __syncwarp();
-  const int n = ctx + t + 1;
-  const float scale = 0.12751743074380304f * ks;  // log2(e) / sqrt(128)
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int p = k0 + lane;
-    float s = -INFINITY;
-    long long cell = -1;
-    if (p < n) {
-      cell = paged_row(pb, kv, b, p, err);
-      s = 0.f;
-      if (cell >= 0) {
-        cell += (long long)g << kv.page_shift;
-        if (FP8) {
-          const uint4* r = reinterpret_cast<const uint4*>(kv.k + cell * 128);
-          for (int i = 0; i < 8; ++i) {
-            const uint4 u = r[i];
-            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-            for (int j = 0; j < 8; ++j) {
-              const float2 f = e4m3x2_to_f32x2((uint16_t)(x[j >> 1] >> (16 * (j & 1))));
-              s += f.x * qs[w][16 * i + 2 * j] + f.y * qs[w][16 * i + 2 * j + 1];
+}
+
+// Walk over the items that meet this CTA's units.
+struct ChunkWalk {
+  const PagedAttn& a;
+  int G, TQ, b, g, p;
+  int q0, n_q, ctx, pairs, odd;  // of the sequence
+  long long before, left;        // units of the item before the CTA's range, units from there on in the range
+  bool pair;
+  int t0, n_keys, nk0, n;  // first token; keys of the item; KV tiles of Q tile 0 (pair), of the item
+  int k0, k1;              // the CTA's KV tiles
+  __device__ ChunkWalk(const PagedAttn& a_, const CtaStart& s, long long units)
+      : a(a_), G(a_.Hq / a_.kv.Hkv), TQ(128 / G), b(s.b), g(s.g), p(s.j), before(s.n_keys), left(units), k0(0), k1(0) {
+    if (left > 0) {
+      set_seq();
+      set_item();
+      if (k0 >= k1) next();
+    }
+  }
+  __device__ bool valid() const { return left > 0; }
+  __device__ void set_seq() {
+    q0 = a.pb.q_start[b];
+    n_q = a.pb.q_start[b + 1] - q0;
+    ctx = a.pb.ctx_len[b];
+    const int tiles = (int)(((long long)n_q * G + 127) / 128);
+    pairs = tiles >> 1;
+    odd = tiles & 1;
+  }
+  __device__ void set_item() {
+    pair = p < pairs;
+    t0 = p * 2 * TQ;
+    n_keys = ctx + min(t0 + (pair ? 2 : 1) * TQ, n_q);
+    n = (n_keys - 1) / kTileK + 1;
+    nk0 = pair ? (ctx + t0 + TQ - 1) / kTileK + 1 : n;
+    const int w = pair ? 2 : 1;
+    k0 = (int)((before + w - 1) / w);
+    k1 = (int)min((long long)n, (before + left + w - 1) / w);
+  }
+  // the next item with tiles in the range, if any
+  __device__ void next() {
+    do {
+      left -= (pair ? 2ll : 1ll) * n - before;
+      if (left <= 0) return;
+      before = 0;
+      if (++p >= pairs + odd) {
+        p = 0;
+        if (++g == a.kv.Hkv) {
+          g = 0;
+          do { ++b; } while (b < a.pb.B && a.plan[b + 1] == a.plan[b]);
+          if (b >= a.pb.B) { left = 0; return; }
+          set_seq();
+        }
+      }
+      set_item();
+    } while (k0 >= k1);
+  }
+  // KV tiles of warpgroup X in the CTA's range: first, step, end
+  __device__ int first(int X) const { return pair ? k0 : k0 + X; }
+  __device__ int step() const { return pair ? 1 : 2; }
+  __device__ int end(int X) const { return pair && X == 0 ? min(k1, nk0) : k1; }
+  __device__ bool any(int X) const { return first(X) < end(X); }
+  __device__ bool loads_q(int X) const { return pair ? any(X) : X == 0; }
+};
+
+template <bool FP8>
+struct ChunkCfg {
+  static constexpr int kThreads = FP8 ? 512 : 384;  // softmax 0, 1; control (K, MMA 0, MMA 1, V); V widening
+  // registers a thread of the softmax, control and widening warpgroups: the sum of the shares must fit
+  // what the block is launched with
+  static constexpr int kRegsSoftmax = FP8 ? 184 : 200, kRegsCtl = FP8 ? 72 : 88, kRegsWiden = 72;
+  static constexpr int kRegBudget = (2 * kRegsSoftmax + kRegsCtl + (FP8 ? kRegsWiden : 0)) * 128;
+  static constexpr uint32_t kQTile = 2 * kTile8;                  // bf16: 2 halves; e4m3: 2 terms
+  static constexpr uint32_t kKTile = FP8 ? kTile8 : 2 * kTile8;
+  static constexpr uint32_t kVTile = 2 * kTile8;                  // 16-bit
+  // even ring depths: warpgroup X's consecutive tiles of a single item are two apart, so a
+  // stage's previous tile is one that the waiting thread has seen (or lies in an item that is over)
+  static constexpr int kKStages = FP8 ? 4 : 2, kVStages = 2, kRaw = FP8 ? 2 : 0;
+  static constexpr uint32_t kOffK = 2 * kQTile;
+  static constexpr uint32_t kOffV = kOffK + kKStages * kKTile;
+  static constexpr uint32_t kOffRaw = kOffV + kVStages * kVTile;  // e4m3 V tiles as loaded
+  static constexpr uint32_t kOffML = kOffRaw + kRaw * kTile8;     // m [128], l [128] of warpgroup 1; q factors [128]
+  static constexpr uint32_t kOffBar = kOffML + 3 * 128 * 4;
+  static constexpr uint32_t kSmem = kOffBar + 40 * 8 + 16 + 1024;
+};
+
+// Tensor memory (512 columns): warpgroup X owns columns [256 X, 256 X + 256): S_X = [256 X, 256 X + 128)
+// (fp32 scores; columns [64, 128) are reused for the 16-bit probabilities), O_X = the other 128.
+template <bool FP8>
+__global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
+    attn_paged_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
+                            const PagedAttn a) {
+  using C = ChunkCfg<FP8>;
+  constexpr int NK = C::kKStages, NV = C::kVStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_full = bars;          // [2] Q tile X written
+  uint64_t* k_full = bars + 2;      // [NK <= 4]
+  uint64_t* k_empty = bars + 6;     // [NK] two arrivals a tile
+  uint64_t* v_full = bars + 10;     // [NV = 2] 16-bit V tile there
+  uint64_t* v_empty = bars + 12;    // [NV] two arrivals a tile
+  uint64_t* raw_full = bars + 14;   // [2] e4m3 V tile loaded
+  uint64_t* raw_empty = bars + 16;  // [2]
+  uint64_t* s_full = bars + 18;     // [2] scores of X ready
+  uint64_t* s_read = bars + 20;     // [2] scores of X in registers
+  uint64_t* p_full = bars + 22;     // [2] P_X written (and O_X rescaled)
+  uint64_t* pv_done = bars + 24;    // [2] P.V of X's tile complete
+  uint64_t* drain = bars + 26;      // [2] an issuer's MMAs complete
+  // both warpgroups and both issuers are through with an item: nobody gets more than one item
+  // ahead, so that no wait can take an older phase of a barrier for the one it means
+  uint64_t* item_done = bars + 28;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 29);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* ml = reinterpret_cast<float*>(smem + C::kOffML);
+  int* err = a.err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&v_full[i], FP8 ? 4 : 1);
+      mbar_init(&v_empty[i], 2);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_read[i], 4);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < NK; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
+    mbar_init(item_done, 8 + 2);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); tma_prefetch_desc(&tmK16); tma_prefetch_desc(&tmV16);
+  }
+  if (warp == 9) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
+  const CtaStart start = a.start[blockIdx.x];
+  const long long U = start.units;
+  const long long units = share(U, blockIdx.x + 1, n_cta) - share(U, blockIdx.x, n_cta);
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ V widening (e4m3 pages)
+    regs_decrease<C::kRegsWiden>();
+    const int t = threadIdx.x - 384;
+    int c = 0;
+    bool ok = true;
+    for (ChunkWalk w(a, start, units); w.valid(); w.next()) {
+      for (int k = w.k0; k < w.k1; ++k, ++c) {
+        const int rs = c & 1, vs = c % NV;
+        const uint32_t rphase = (uint32_t)((c >> 1) & 1), vphase = (uint32_t)((c / NV) & 1);
+        ok = ok && !*s_abort && mbar_wait(&raw_full[rs], rphase, err) && mbar_wait(&v_empty[vs], vphase ^ 1u, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        const uint8_t* src = smem + C::kOffRaw + rs * kTile8;
+        uint8_t* dst = smem + C::kOffV + vs * C::kVTile;
+        const int valid = w.n_keys - k * kTileK;  // rows past the last key become zero (0 * NaN would poison O)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 16 + (t >> 3), ch = t & 7;  // 16 dims [16 ch, 16 ch + 16) of a row
+          uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ((ch ^ (row & 7)) << 4));
+          if (row >= valid) u = make_uint4(0, 0, 0, 0);
+          uint4 lo, hi;
+          lo.x = e4m3x2_to_f16x2((uint16_t)u.x); lo.y = e4m3x2_to_f16x2((uint16_t)(u.x >> 16));
+          lo.z = e4m3x2_to_f16x2((uint16_t)u.y); lo.w = e4m3x2_to_f16x2((uint16_t)(u.y >> 16));
+          hi.x = e4m3x2_to_f16x2((uint16_t)u.z); hi.y = e4m3x2_to_f16x2((uint16_t)(u.z >> 16));
+          hi.z = e4m3x2_to_f16x2((uint16_t)u.w); hi.w = e4m3x2_to_f16x2((uint16_t)(u.w >> 16));
+          uint8_t* d = dst + (ch >> 2) * kTile8 + row * 128;
+          const int c2 = 2 * (ch & 3);
+          *reinterpret_cast<uint4*>(d + ((c2 ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ (row & 7)) << 4)) = hi;
+        }
+        fence_proxy_async_smem();
+        arrive_warp(&v_full[vs], lane);
+        if (lane == 0) mbar_arrive(&raw_empty[rs]);
+      }
+    }
+    if (!ok) *s_abort = 1;
+  } else if (warp >= 8) {
+    regs_decrease<C::kRegsCtl>();
+    if (warp == 8 || warp == 11) {
+      // -------------------------------------------------------- TMA producers: K; V
+      // As in the decode form: lane i finds box i's page a tile ahead, one lane issues.
+      const bool is_v = warp == 11;
+      const CUtensorMap* map = is_v ? &tmV : &tmK;
+      const CUtensorMap* map16 = is_v ? &tmV16 : &tmK16;
+      uint64_t* full = is_v ? (FP8 ? raw_full : v_full) : k_full;
+      uint64_t* empty = is_v ? (FP8 ? raw_empty : v_empty) : k_empty;
+      const int ns = is_v ? 2 : NK;
+      uint8_t* ring = smem + (is_v ? (FP8 ? C::kOffRaw : C::kOffV) : C::kOffK);
+      const int shift = a.kv.page_shift, in_page = (1 << shift) - 1, box_shift = min(shift, 7);
+      const int n_pages = a.kv.n_pages, rows_all = (n_pages * Hkv) << shift;
+      ChunkWalk w(a, start, units);
+      int k = w.k0;
+      auto look_up = [&]() {
+        const int rest = w.n_keys - k * kTileK;
+        const int off = lane << (rest >= kTileK ? box_shift : 4);
+        if (off >= kTileK || off >= rest) return 0;
+        return __ldg(a.pb.table + (long long)w.b * a.pb.max_pages + ((k * kTileK + off) >> shift));
+      };
+      int page = w.valid() ? look_up() : 0;
+      int st = 0, done = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (w.valid()) {
+        const int g = w.g, kv0 = k * kTileK, rest = w.n_keys - kv0;
+        const bool tail = rest < kTileK;
+        const int bs = tail ? 4 : box_shift;
+        const int n = tail ? (rest + 15) >> 4 : kTileK >> bs;
+        // a bad page reads as zeros: behind the tensor map's last row
+        const bool in = (unsigned)page < (unsigned)n_pages;
+        if (!in) record_error(err, kErrInvalid);
+        const int my_row = in ? ((page * Hkv + g) << shift) + ((kv0 + (lane << bs)) & in_page) : rows_all;
+        int row[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, my_row, i);
+        if (++k == w.k1) {
+          w.next();
+          k = w.k0;
+        }
+        if (w.valid()) page = look_up();
+        ok = !*s_abort && mbar_wait(&empty[st], phase ^ 1u, err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        uint8_t* dst = ring + st * (FP8 ? kTile8 : 2 * kTile8);
+        if (elect_one()) {
+          const CUtensorMap* m = tail ? map16 : map;
+          mbar_arrive_expect_tx(&full[st], (n << bs) * 128 * (FP8 ? 1 : 2));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < n) {
+              tma_load_2d(dst + ((i << bs) * 128), m, &full[st], 0, row[i]);
+              if (!FP8) tma_load_2d(dst + kTile8 + ((i << bs) * 128), m, &full[st], 64, row[i]);
             }
+        }
+        __syncwarp();
+        ++done;
+        if (++st == ns) { st = 0; phase ^= 1u; }
+      }
+      if (!ok) {
+        *s_abort = 1;
+        // let the copies still in flight land before the CTA exits
+        for (int i = done > ns ? done - ns : 0; i < done; ++i) mbar_wait(&full[i % ns], (uint32_t)((i / ns) & 1), err);
+      }
+    } else if (lane == 0) {
+      // --------------------------------------------------- MMA issuers, one per warpgroup X
+      const int X = warp - 9;
+      constexpr uint32_t idesc_s = FP8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
+      constexpr uint32_t idesc_o = FP8 ? idesc_f16_f32(128, kD, 0, 1) : idesc_bf16_f32(128, kD, 0, 1);
+      int c0 = 0, u = 0, q_loads[2] = {0, 0}, it = 0;
+      bool ok = true;
+      for (ChunkWalk w(a, start, units); w.valid() && ok; w.next(), ++it) {
+        if (it > 0) {
+          ok = !*s_abort && mbar_wait(item_done, (uint32_t)((it - 1) & 1), err);
+          if (!ok) break;
+        }
+        const int kb = w.first(X), ke = w.end(X), step = w.step();
+        const int qt = w.pair ? X : 0;  // the Q tile
+        const uint32_t qa = smem_u32(smem) + qt * C::kQTile;
+        q_loads[0] += w.loads_q(0);
+        q_loads[1] += w.loads_q(1);
+        // arrivals this issuer owes a stage: its own, and the other's where that one skips the tile
+        auto arrivals = [&](int k) { return !w.pair || (X == 1 && k >= w.nk0) ? 2 : 1; };
+        // S_X of tile k in two N = 64 halves: keys [0, 64) may go to columns [0, 64) as soon as
+        // the softmax has read the previous scores; columns [64, 128) hold P until its P.V is
+        // complete
+        auto issue_s_half = [&](int k, int h) -> bool {
+          const int c = c0 + (k - w.k0), st = c % NK;
+          if (*s_abort || !mbar_wait(&k_full[st], (uint32_t)((c / NK) & 1), err)) return false;
+          tc_fence_after();
+          const uint32_t sk = smem_u32(smem + C::kOffK + st * C::kKTile) + h * 64 * 128;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t ad = sdesc_kmajor_sw128(qa + (kk >> 2) * kTile8) + 2 * (kk & 3);
+            if (FP8)  // both terms of q against the same K
+              mma_e4m3_ss(tmem + 256 * X + 64 * h, ad, sdesc_kmajor_sw128(sk) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
+            else
+              mma_bf16_ss(tmem + 256 * X + 64 * h, ad, sdesc_kmajor_sw128(sk + (kk >> 2) * kTile8) + 2 * (kk & 3),
+                          idesc_s, kk ? 1u : 0u);
           }
-        } else {
-          const uint4* r = reinterpret_cast<const uint4*>(kv.k + cell * 256);
-          for (int i = 0; i < 16; ++i) {
-            const uint4 u = r[i];
-            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-            for (int j = 0; j < 4; ++j)
-              s += bf16_lo(x[j]) * qs[w][8 * i + 2 * j] + bf16_hi(x[j]) * qs[w][8 * i + 2 * j + 1];
+          if (h == 1) {
+            mma_commit(&s_full[X]);
+            for (int i = arrivals(k); i > 0; --i) mma_commit(&k_empty[st]);
+          }
+          return true;
+        };
+        if (kb < ke) {
+          ok = !*s_abort && mbar_wait(&q_full[qt], (uint32_t)((q_loads[qt] - 1) & 1), err);
+          // the scores of the previous item are read and its P.V complete
+          if (ok && u > 0)
+            ok = mbar_wait(&s_read[X], (uint32_t)((u - 1) & 1), err) &&
+                 mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
+          if (ok) {
+            tc_fence_after();
+            ok = issue_s_half(kb, 0) && issue_s_half(kb, 1);
           }
         }
-        s *= scale;
+        for (int k = kb; k < ke && ok; k += step, ++u) {
+          const bool more = k + step < ke;
+          const uint32_t par = (uint32_t)(u & 1);
+          if (more) {
+            if (*s_abort || !mbar_wait(&s_read[X], par, err)) { ok = false; break; }
+            tc_fence_after();
+            if (!issue_s_half(k + step, 0)) { ok = false; break; }
+          }
+          const int c = c0 + (k - w.k0), st = c % NV;
+          if (*s_abort || !mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err) || !mbar_wait(&p_full[X], par, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sv = smem_u32(smem + C::kOffV + st * C::kVTile);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + 256 * X + 128, tmem + 256 * X + 64 + kk * 8,
+                        sdesc_mnmajor_sw128(sv + kk * 16 * 128, kTile8, 1024), idesc_o, (k != kb || kk) ? 1u : 0u);
+          mma_commit(&pv_done[X]);
+          for (int i = arrivals(k); i > 0; --i) mma_commit(&v_empty[st]);
+          if (more) {
+            if (*s_abort || !mbar_wait(&pv_done[X], par, err)) { ok = false; break; }
+            tc_fence_after();
+            if (!issue_s_half(k + step, 1)) { ok = false; break; }
+          }
+        }
+        c0 += w.k1 - w.k0;
+        mbar_arrive(item_done);
       }
+      if (!ok) *s_abort = 1;
+      mma_commit(&drain[X]);  // every MMA completes before the tensor memory is released
+      mbar_wait(&drain[X], 0, err);
     }
-    const float mn = fmaxf(m, warp_max(s));
-    const float pr = s == -INFINITY ? 0.f : exp2f(s - mn);
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
-    m = mn;
-    l = l * alpha + warp_sum(pr);
-    for (int i = 0; i < 4; ++i) o[i] *= alpha;
-    const int nk = min(32, n - k0);
-    for (int j = 0; j < nk; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, pr, j);
-      const long long c = __shfl_sync(0xffffffffu, cell, j);
-      if (c < 0) continue;
-      if (FP8) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(kv.v + c * 128 + 4 * lane);
-        const float2 a = e4m3x2_to_f32x2((uint16_t)u), e = e4m3x2_to_f32x2((uint16_t)(u >> 16));
-        o[0] += pj * a.x; o[1] += pj * a.y; o[2] += pj * e.x; o[3] += pj * e.y;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(kv.v + c * 256 + 8 * lane);
-        o[0] += pj * bf16_lo(u.x); o[1] += pj * bf16_hi(u.x); o[2] += pj * bf16_lo(u.y); o[3] += pj * bf16_hi(u.y);
+  } else {
+    regs_increase<C::kRegsSoftmax>();
+    // ---------------------------------------------------------------- softmax
+    const int X = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;  // row of the Q tile, tensor-memory lane
+    const int G = a.Hq / Hkv, TQ = 128 / G;
+    const uint32_t tS = tmem + 256 * X + ((uint32_t)(quad * 32) << 16), tO = tS + 128;
+    // fp16 probabilities: the running maximum is kept 7 below the scores', so that P <= 2^15
+    constexpr float kShift = FP8 ? 7.f : 0.f;
+    int c0 = 0, u = 0, q_loads0 = 0, it = 0;
+    bool ok = true;
+    ChunkMeta meta = {};
+    for (ChunkWalk w(a, start, units); w.valid(); w.next(), ++it) {
+      const int qt = w.pair ? X : 0, tile_t0 = w.t0 + qt * TQ;
+      const int n_rows = min(TQ, w.n_q - tile_t0) * G;
+      const bool valid = r < n_rows;
+      const bool warp_valid = quad * 32 < n_rows;
+      const int tok = w.q0 + tile_t0 + r / G, head = w.g * G + r % G;
+      const int qpos = valid ? w.ctx + tile_t0 + r / G : w.n_keys - 1;
+      q_loads0 += w.loads_q(0);
+      float factor = kScaleLog2;
+      if (w.loads_q(X)) {
+        // this thread's row of Q tile X into shared memory, 128-byte swizzle (zeros behind the last)
+        uint8_t* dst = smem + X * C::kQTile + r * 128;
+        uint4 v[16];
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)tok * a.ldq + (long long)head * kD);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        if (!FP8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * kTile8 + (((i & 7) ^ (r & 7)) << 4)) = v[i];
+        } else {
+          // q = 2^e (t1 + t2), the largest value scaled into [128, 256)
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx = max(mx, max(x[j] & 0x7fffu, (x[j] >> 16) & 0x7fffu));
+          }
+          const int ex = (int)(mx >> 7);
+          const int e = min(max(ex - 127 - 7, -119), 119);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          factor = ex == 255 ? __uint_as_float(0x7fc00000u)
+                             : kScaleLog2 * a.kv.k_scale[w.g] * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // 16 values
+            uint32_t t1[4], t2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4& vv = v[2 * i + (j >> 1)];
+              const uint32_t x0 = j & 1 ? vv.z : vv.x, x1 = j & 1 ? vv.w : vv.y;
+              const float f0 = bf16_lo(x0) * down, f1 = bf16_hi(x0) * down, f2 = bf16_lo(x1) * down,
+                          f3 = bf16_hi(x1) * down;
+              const uint16_t p0 = pack_e4m3x2(f0, f1), p1 = pack_e4m3x2(f2, f3);
+              const float2 b0 = e4m3x2_to_f32x2(p0), b1 = e4m3x2_to_f32x2(p1);
+              t1[j] = p0 | ((uint32_t)p1 << 16);
+              t2[j] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | ((uint32_t)pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+            }
+            uint8_t* d = dst + ((i ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+            *reinterpret_cast<uint4*>(d + kTile8) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          }
+          if (!w.pair) ml[256 + r] = factor;  // for warpgroup 1
+        }
+        fence_proxy_async_smem();
+        arrive_warp(&q_full[X], lane);
+      } else if (FP8 && w.any(X)) {
+        ok = ok && !*s_abort && (it == 0 || mbar_wait(item_done, (uint32_t)((it - 1) & 1), err)) &&
+             mbar_wait(&q_full[0], (uint32_t)((q_loads0 - 1) & 1), err);
+        ok = __all_sync(0xffffffffu, ok);
+        factor = ml[256 + r];
       }
+      float m_run = -INFINITY, l_run = 0.f;
+      const int kb = w.first(X), ke = w.end(X), step = w.step();
+      for (int k = kb; k < ke; k += step, ++u) {
+        const uint32_t par = (uint32_t)(u & 1);
+        ok = ok && !*s_abort && mbar_wait(&s_full[X], par, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
+          tc_fence_before();
+          arrive_warp(&s_read[X], lane);
+          if (!FP8 && ok && k * kTileK + kTileK > w.n_keys) {
+            const int c = c0 + (k - w.k0), st = c % NV;
+            ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
+            if (ok && k * kTileK + r >= w.n_keys) {
+              uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          arrive_warp(&p_full[X], lane);
+          continue;
+        }
+        tc_fence_after();
+        const int kv0 = k * kTileK;
+        const bool need_mask = __any_sync(0xffffffffu, kv0 + kTileK - 1 > qpos);
+        // the whole 128-column score row of this thread in one tensor-memory round trip
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(v[c]);
+        tc_fence_before();
+        arrive_warp(&s_read[X], lane);  // columns [0, 64) of S_X may now take the next tile's scores
+        if (need_mask) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (kv0 + c * 32 + i > qpos) v[c][i] = __float_as_uint(-INFINITY);
+        }
+        float mc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mc[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+          for (int i = 1; i < 31; i += 2) mc[c] = fmax3(mc[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+          mc[c] = fmaxf(mc[c], __uint_as_float(v[c][31]));
+        }
+        const float mxs = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * factor - kShift;
+        float alpha = 1.f;
+        if (mxs > m_run + kRescaleThreshold || m_run == -INFINITY) {
+          alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mxs);
+          m_run = mxs;
+        }
+        // p = 2^(s factor - m); a row that has seen no key yet (its causal limit lies before
+        // this tile) keeps m = -inf and p = 2^-inf = 0
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+        const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
+        const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
+        uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t e = f2_fma(f2_pack(v[c][i], v[c][i + 1]), scale2, neg2);
+            const float p0 = ex2_approx(f2_lo(e));
+            const float p1 = ex2_approx(f2_hi(e));
+            acc2[(i >> 1) & 1] = f2_add(acc2[(i >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+            v[c][i >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + 64 + c * 16, v[c]);
+        }
+        const uint64_t acc = f2_add(acc2[0], acc2[1]);
+        l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
+        // O_X is stable here: the second half of S_X was issued only after the previous P.V completed
+        if (k > kb && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+        }
+        // bf16 V: zero the rows past the last key (0 * NaN would poison O); both warpgroups
+        // of a pair do so before they release their P (the second writes zeros over zeros)
+        if (!FP8 && kv0 + kTileK > w.n_keys) {
+          const int c = c0 + (k - w.k0), st = c % NV;
+          ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
+          if (ok && kv0 + r >= w.n_keys) {
+            uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&p_full[X], lane);
+      }
+      c0 += w.k1 - w.k0;
+      const bool any = kb < ke;
+      if (any) {
+        ok = ok && !*s_abort && mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      // a single item's other half: warpgroup 1 leaves m, l in shared memory and O_1 in place
+      float w0 = 1.f, w1 = 0.f;
+      bool other = false;
+      if (!w.pair) {
+        if (X == 1) {
+          ml[r] = any ? m_run : -INFINITY;
+          ml[128 + r] = l_run;
+        }
+        tc_fence_before();
+        named_bar(1, 256);
+        tc_fence_after();
+        if (X == 0) {
+          const float m1 = ml[r], M = fmaxf(m_run, m1);
+          other = w.any(1);
+          if (other && M != -INFINITY) {
+            w0 = ex2_approx(m_run - M);
+            w1 = ex2_approx(m1 - M);
+            l_run = l_run * w0 + ml[128 + r] * w1;
+            m_run = M;
+          }
+        }
+      }
+      const int nk = w.pair && X == 0 ? w.nk0 : w.n;  // KV tiles of this Q tile
+      const bool writes = any && (w.pair || X == 0);
+      if (writes && warp_valid && ok) {
+        tc_fence_after();
+        const bool whole = w.k0 == 0 && w.k1 >= nk;
+        const float vs = FP8 ? a.kv.v_scale[w.g] : 1.f;
+        const float mul = whole ? vs / l_run : 1.f;
+        uint16_t* dst = a.out + (long long)tok * a.ldo + (long long)head * kD;
+        float* part = a.part + ((long long)(blockIdx.x * 2 + (w.k0 > 0 ? 0 : 1)) * 2 + X) * kChunkPart;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld_regs(o);
+          if (other) {  // the same for all threads
+            uint32_t o1[32];
+            tmem_ld32(tO + 256 + c * 32, o1);
+            tmem_wait_ld_regs(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + (w1 != 0.f ? __uint_as_float(o1[i]) * w1 : 0.f));
+          }
+          if (valid && whole) {
+            const bool f16 = a.o_f16 != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 q;
+              q.x = pack_op_x2(f16, __uint_as_float(o[8 * i + 0]) * mul, __uint_as_float(o[8 * i + 1]) * mul);
+              q.y = pack_op_x2(f16, __uint_as_float(o[8 * i + 2]) * mul, __uint_as_float(o[8 * i + 3]) * mul);
+              q.z = pack_op_x2(f16, __uint_as_float(o[8 * i + 4]) * mul, __uint_as_float(o[8 * i + 5]) * mul);
+              q.w = pack_op_x2(f16, __uint_as_float(o[8 * i + 6]) * mul, __uint_as_float(o[8 * i + 7]) * mul);
+              *reinterpret_cast<uint4*>(dst + c * 32 + i * 8) = q;
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(part + (c * 32 + i) * 128 + r, __uint_as_float(o[i]));
+          }
+          __syncwarp();
+        }
+        if (!whole && valid) {
+          __stcg(part + kD * 128 + r, m_run);
+          __stcg(part + kD * 128 + 128 + r, l_run);
+        }
+      }
+      if (writes && ok) {
+        if (w.k0 > 0) meta.has = 1;
+        if (w.k0 == 0 && w.k1 < nk) {
+          const int wgt = w.pair ? 2 : 1;
+          const long long us = share(U, blockIdx.x, n_cta) + (units - w.left);  // the item's first unit
+          meta.split = 1;
+          meta.c_last = cta_of(us + (long long)wgt * (nk - 1), U, n_cta);
+          meta.n_rows = n_rows;
+          meta.tok = w.q0 + tile_t0;
+          meta.g = w.g;
+        }
+      }
+      if (!w.pair) named_bar(1, 256);  // O_1, m and l are read
+      arrive_warp(item_done, lane);
+    }
+    if (!ok) *s_abort = 1;
+    if (r == 0) a.meta[blockIdx.x * 2 + X] = meta;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of the Q tiles that span CTAs: blocks (c, X, 16 dims) with the tiles that
+// CTA c began and did not end. o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M) over the CTAs in order.
+__global__ void __launch_bounds__(128) paged_chunk_join_kernel(const PagedAttn a) {
+  pdl_wait();
+  pdl_trigger();
+  const int cx = blockIdx.x >> 3, d0 = (blockIdx.x & 7) * 16, c = cx >> 1, X = cx & 1;
+  const ChunkMeta m = a.meta[cx];
+  const int r = threadIdx.x;
+  if (!m.split || r >= m.n_rows) return;
+  auto part = [&](int i) { return a.part + ((long long)(i * 2 + (i == c ? 1 : 0)) * 2 + X) * kChunkPart; };
+  auto has = [&](int i) { return i == c || a.meta[i * 2 + X].has != 0; };
+  float M = -INFINITY;
+  for (int i = c; i <= m.c_last; ++i)
+    if (has(i)) M = fmaxf(M, __ldcg(part(i) + kD * 128 + r));
+  float L = 0.f, o[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll 4
+  for (int i = c; i <= m.c_last; ++i) {
+    if (!has(i)) continue;
+    const float* p = part(i);
+    const float mi = __ldcg(p + kD * 128 + r), li = __ldcg(p + kD * 128 + 128 + r);
+    const float w = mi == -INFINITY ? 0.f : exp2f(mi - M);
+    L += li * w;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float v = __ldcg(p + (d0 + j) * 128 + r);
+      o[j] += w != 0.f ? v * w : 0.f;
     }
   }
-  const float inv = vs / l;
-  uint2 r;
-  r.x = pack_op_x2(o_f16 != 0, o[0] * inv, o[1] * inv);
-  r.y = pack_op_x2(o_f16 != 0, o[2] * inv, o[3] * inv);
-  *reinterpret_cast<uint2*>(out + tok * ldo + (long long)h * 128 + 4 * lane) = r;
+  const int G = a.Hq / a.kv.Hkv;
+  const float mul = (a.kv.fp8 ? a.kv.v_scale[m.g] : 1.f) / L;
+  uint16_t* dst = a.out + (long long)(m.tok + r / G) * a.ldo + (long long)(m.g * G + r % G) * kD + d0;
+  const bool f16 = a.o_f16 != 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 q;
+    q.x = pack_op_x2(f16, o[8 * h] * mul, o[8 * h + 1] * mul);
+    q.y = pack_op_x2(f16, o[8 * h + 2] * mul, o[8 * h + 3] * mul);
+    q.z = pack_op_x2(f16, o[8 * h + 4] * mul, o[8 * h + 5] * mul);
+    q.w = pack_op_x2(f16, o[8 * h + 6] * mul, o[8 * h + 7] * mul);
+    *reinterpret_cast<uint4*>(dst + 8 * h) = q;
+  }
 }
 
 // ----------------------------------------------------------------------------
@@ -937,20 +1622,21 @@ __global__ void __launch_bounds__(128) attn_paged_simple_kernel(const PagedBatch
 // ----------------------------------------------------------------------------
 namespace {
 
-// Scratch of a call, in order: work list, CTA starts, merge counters, partials, e4m3 query terms and scales.
+// Scratch of a call, in order: work list, CTA starts, merge counters (decode form) or what the CTAs
+// leave to join (chunk form), partials, e4m3 query terms and scales.
 struct Scratch {
   size_t plan, start, counters, part, q8, q8_scale, bytes;
 };
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 Scratch scratch_of(int B, int Hq, int Hkv, int max_q) {
   Scratch s;
+  const bool decode = max_q == 1;
+  const size_t G = Hq / Hkv, rows = (size_t)B * Hkv;
   s.plan = 0;
   s.start = s.plan + up256(((size_t)B + 1) * sizeof(long long));
   s.counters = s.start + kMaxCtas * sizeof(CtaStart);
-  const bool decode = max_q == 1;
-  const int G = Hq / Hkv;
-  s.part = s.counters + up256(decode ? (size_t)B * Hkv * sizeof(int) : 256);
-  s.q8 = s.part + up256(decode ? ((size_t)B * Hkv + kMaxCtas) * G * kPartFloats * sizeof(float) : 256);
+  s.part = s.counters + up256(decode ? rows * sizeof(int) : 2 * kChunkCtas * sizeof(ChunkMeta));
+  s.q8 = s.part + up256((decode ? (rows + kMaxCtas) * G * kPartFloats : (size_t)4 * kChunkCtas * kChunkPart) * sizeof(float));
   s.q8_scale = s.q8 + up256(decode ? (size_t)B * Hq * 2 * kD : 0);
   s.bytes = s.q8_scale + up256(decode ? (size_t)B * Hq * sizeof(float) : 0);
   return s;
@@ -1007,6 +1693,28 @@ int attention_decode(const PagedAttn& a, cudaStream_t s) {
   return -2;
 }
 
+template <bool FP8>
+int attention_chunk(const PagedAttn& a, cudaStream_t s) {
+  using C = ChunkCfg<FP8>;
+  CUtensorMap tmK, tmV, tmK16, tmV16;
+  if (page_maps(a.kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
+  auto kernel = attn_paged_chunk_kernel<FP8>;
+  bool first = false;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem, &first)) return -6;
+  if (first) {
+    // the register split must fit what the block is launched with, or the increase never returns
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs * C::kThreads < C::kRegBudget) {
+      set_last_error("attention_paged: chunk kernel built with too few registers for its warpgroup split");
+      return -6;
+    }
+  }
+  q3_launch(paged_chunk_plan_kernel, 1, kPlanThreads, 0, s, a);
+  q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmK, tmV, tmK16, tmV16, a);
+  q3_launch(paged_chunk_join_kernel, a.n_cta * 16, 128, 0, s, a);
+  return 0;
+}
+
 }  // namespace
 
 size_t paged_attention_bytes(int B, int Hq, int Hkv, int max_q) { return scratch_of(B, Hq, Hkv, max_q).bytes; }
@@ -1024,24 +1732,15 @@ int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int m
   a.out = out; a.ldo = ldo;
   a.plan = reinterpret_cast<long long*>(base + off.plan);
   a.start = reinterpret_cast<CtaStart*>(base + off.start);
-  a.n_cta = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  const int cap = max_q == 1 ? kMaxCtas : kChunkCtas;
+  a.n_cta = num_sms() < cap ? num_sms() : cap;
+  a.meta = reinterpret_cast<ChunkMeta*>(base + off.counters);
   a.counters = reinterpret_cast<int*>(base + off.counters);
   a.part = reinterpret_cast<float*>(base + off.part);
   a.q8 = base + off.q8;
   a.q8_scale = reinterpret_cast<float*>(base + off.q8_scale);
   a.err = err;
-  int rc = 0;
-  if (max_q == 1) {
-    rc = attention_decode(a, s);
-  } else {
-    const long long blocks = ((long long)n_tokens * Hq + 3) / 4;
-    if (blocks >= (1ll << 31)) {
-      set_last_error("attention_paged: %d tokens exceed the grid limit", n_tokens);
-      return -2;
-    }
-    q3_launch(kv.fp8 ? attn_paged_simple_kernel<true> : attn_paged_simple_kernel<false>, (unsigned)blocks, 128, 0, s,
-              pb, kv, Hq, n_tokens, max_q, q, ldq, out, ldo, o_f16 ? 1 : 0, err);
-  }
+  const int rc = max_q == 1 ? attention_decode(a, s) : kv.fp8 ? attention_chunk<true>(a, s) : attention_chunk<false>(a, s);
   if (rc) return rc;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
