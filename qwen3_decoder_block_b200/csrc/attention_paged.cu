@@ -1069,7 +1069,8 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
   // both warpgroups and both issuers are through with an item: nobody gets more than one item
   // ahead, so that no wait can take an older phase of a barrier for the one it means
   uint64_t* item_done = bars + 28;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 29);
+  uint64_t* turn = bars + 29;       // [2] pairs: warpgroup X may start its exponentials
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* ml = reinterpret_cast<float*>(smem + C::kOffML);
   int* err = a.err;
@@ -1087,6 +1088,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drain[i], 1);
+      mbar_init(&turn[i], 4);
     }
     for (int i = 0; i < NK; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
     mbar_init(item_done, 8 + 2);
@@ -1307,6 +1309,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     // fp16 probabilities: the running maximum is kept 7 below the scores', so that P <= 2^15
     constexpr float kShift = FP8 ? 7.f : 0.f;
     int c0 = 0, u = 0, q_loads0 = 0, it = 0;
+    int turns = 0;  // the other warpgroup's tiles of pairs so far
     bool ok = true;
     ChunkMeta meta = {};
     for (ChunkWalk w(a, start, units); w.valid(); w.next(), ++it) {
@@ -1380,6 +1383,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
           tc_fence_before();
           arrive_warp(&s_read[X], lane);
+          if (w.pair) arrive_warp(&turn[X ^ 1], lane);
           if (!FP8 && ok && k * kTileK + kTileK > w.n_keys) {
             const int c = c0 + (k - w.k0), st = c % NV;
             ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
@@ -1431,6 +1435,13 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
         const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
         uint64_t acc2[2] = {0ull, 0ull};
+        // The warpgroups of a pair take turns on the exponentials (the special-function unit
+        // bounds the softmax), so that each turn overlaps the tensor core's work on the other
+        // Q tile: tile k of 0 goes after tile k - 1 of 1, tile k of 1 after tile k of 0 (if 0 has it).
+        if (w.pair && (X == 0 ? k > kb : k < w.end(0))) {
+          const int n = turns + (k - kb) - (X == 0 ? 1 : 0);
+          ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&turn[X], (uint32_t)(n & 1), err));
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -1443,6 +1454,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
           }
           tmem_st16(tS + 64 + c * 16, v[c]);
         }
+        if (w.pair) arrive_warp(&turn[X ^ 1], lane);
         const uint64_t acc = f2_add(acc2[0], acc2[1]);
         l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
         // O_X is stable here: the second half of S_X was issued only after the previous P.V completed
@@ -1474,6 +1486,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         arrive_warp(&p_full[X], lane);
       }
       c0 += w.k1 - w.k0;
+      if (w.pair) turns += max(w.end(X ^ 1) - w.first(X ^ 1), 0);
       const bool any = kb < ke;
       if (any) {
         ok = ok && !*s_abort && mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
