@@ -36,7 +36,7 @@ struct ChunkMeta;
 struct PagedAttn {
   PagedBatch pb;
   KvPages kv;
-  int n_tokens, max_q, Hq, o_f16;
+  int n_tokens, max_q, Hq, g_shift, o_f16;  // g_shift: log2 of the query heads per KV group
   const uint16_t* q;
   long long ldq;
   uint16_t* out;
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 // by a kernel that follows.
 //
 // e4m3 pages: S takes K as it is (kind::f8f6f4) against q split into two e4m3 terms of one
-// scale (exact for bf16 values down to 2^-10 of the row's largest; below, off by at most 2^-18
+// scale (exact for bf16 values down to 2^-10 of the row's largest; below, off by at most 2^-17
 // of it). For P.V a third warpgroup widens V to fp16 in shared memory, which is exact, and P is
 // fp16 scaled to at most 2^15: 2^-11 of each weight, or 2^-31 of the row's largest, is finer
 // than bf16, and one cvt widens two values.
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 namespace {
 
 constexpr int kChunkCtas = 152;                       // grid bound (partials are sized by it)
-constexpr int kChunkPart = kD * 128 + 2 * 128;        // o [128 dims][128 rows], m [128], l [128]
+constexpr int kChunkPart = kD * 128 + 2 * 128;        // o [32][128 rows][4 dims], m [128], l [128]
 
 struct ChunkMeta {
   int split;   // the CTA's last item of warpgroup X goes on in other CTAs
@@ -897,8 +897,8 @@ __device__ __forceinline__ long long pair_tiles(int ctx, int n_q, int s, int P) 
 struct ChunkSeq {
   int n_q, ctx, s, pairs, odd;
   long long head_units;  // of one KV head
-  __device__ ChunkSeq(int nq, int c, int G) : n_q(nq), ctx(c), s(256 / G) {
-    const int tiles = (int)(((long long)nq * G + 127) / 128);
+  __device__ ChunkSeq(int nq, int c, int g_shift) : n_q(nq), ctx(c), s(256 >> g_shift) {
+    const int tiles = (int)((((long long)nq << g_shift) + 127) >> 7);
     pairs = tiles >> 1;
     odd = tiles & 1;
     head_units = 2 * pair_tiles(ctx, n_q, s, pairs) + (odd ? ((long long)ctx + n_q - 1) / kTileK + 1 : 0);
@@ -913,13 +913,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_chunk_plan_kernel(const Pa
   pdl_trigger();
   __shared__ long long wsum[kPlanThreads / 32];
   __shared__ long long plan_s[kPlanShared];
-  const int B = a.pb.B, Hkv = a.kv.Hkv, G = a.Hq / Hkv;
+  const int B = a.pb.B, Hkv = a.kv.Hkv;
   long long carry = 0;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int b = base + (int)threadIdx.x;
     long long v = 0, total;
     int n_q, ctx;
-    if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err) && n_q > 0) v = Hkv * ChunkSeq(n_q, ctx, G).head_units;
+    if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err) && n_q > 0) v = Hkv * ChunkSeq(n_q, ctx, a.g_shift).head_units;
     const long long at = block_prefix(v, wsum, &total);
     if (b < B) a.plan[b] = carry + at;
     if (b < kPlanShared) plan_s[b] = carry + at;
@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_chunk_plan_kernel(const Pa
         if (plan[mid] <= t) lo = mid; else hi = mid - 1;
       }
       s.b = lo;
-      const ChunkSeq q(a.pb.q_start[lo + 1] - a.pb.q_start[lo], a.pb.ctx_len[lo], G);
+      const ChunkSeq q(a.pb.q_start[lo + 1] - a.pb.q_start[lo], a.pb.ctx_len[lo], a.g_shift);
       long long r = t - plan[lo];
       s.g = (int)(r / q.head_units);
       r -= s.g * q.head_units;
@@ -962,14 +962,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_chunk_plan_kernel(const Pa
 // Walk over the items that meet this CTA's units.
 struct ChunkWalk {
   const PagedAttn& a;
-  int G, TQ, b, g, p;
+  int TQ, b, g, p;
   int q0, n_q, ctx, pairs, odd;  // of the sequence
   long long before, left;        // units of the item before the CTA's range, units from there on in the range
   bool pair;
   int t0, n_keys, nk0, n;  // first token; keys of the item; KV tiles of Q tile 0 (pair), of the item
   int k0, k1;              // the CTA's KV tiles
   __device__ ChunkWalk(const PagedAttn& a_, const CtaStart& s, long long units)
-      : a(a_), G(a_.Hq / a_.kv.Hkv), TQ(128 / G), b(s.b), g(s.g), p(s.j), before(s.n_keys), left(units), k0(0), k1(0) {
+      : a(a_), TQ(128 >> a_.g_shift), b(s.b), g(s.g), p(s.j), before(s.n_keys), left(units), k0(0), k1(0) {
     if (left > 0) {
       set_seq();
       set_item();
@@ -981,7 +981,7 @@ struct ChunkWalk {
     q0 = a.pb.q_start[b];
     n_q = a.pb.q_start[b + 1] - q0;
     ctx = a.pb.ctx_len[b];
-    const int tiles = (int)(((long long)n_q * G + 127) / 128);
+    const int tiles = (int)((((long long)n_q << a.g_shift) + 127) >> 7);
     pairs = tiles >> 1;
     odd = tiles & 1;
   }
@@ -989,11 +989,11 @@ struct ChunkWalk {
     pair = p < pairs;
     t0 = p * 2 * TQ;
     n_keys = ctx + min(t0 + (pair ? 2 : 1) * TQ, n_q);
-    n = (n_keys - 1) / kTileK + 1;
-    nk0 = pair ? (ctx + t0 + TQ - 1) / kTileK + 1 : n;
-    const int w = pair ? 2 : 1;
-    k0 = (int)((before + w - 1) / w);
-    k1 = (int)min((long long)n, (before + left + w - 1) / w);
+    n = ((n_keys - 1) >> 7) + 1;
+    nk0 = pair ? ((ctx + t0 + TQ - 1) >> 7) + 1 : n;
+    const int w = pair ? 1 : 0;  // log2 of a tile's units
+    k0 = (int)((before + w) >> w);
+    k1 = (int)min((long long)n, (before + left + w) >> w);
   }
   // the next item with tiles in the range, if any
   __device__ void next() {
@@ -1020,6 +1020,19 @@ struct ChunkWalk {
   __device__ bool any(int X) const { return first(X) < end(X); }
   __device__ bool loads_q(int X) const { return pair ? any(X) : X == 0; }
 };
+
+// 16 bytes of global memory, or zeros. Volatile: the compiler keeps a run of these together (it
+// would sink plain loads to their uses, one latency each).
+__device__ __forceinline__ uint4 ld_or_zero(const void* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p), "r"((int)there));
+  return v;
+}
 
 template <bool FP8>
 struct ChunkCfg {
@@ -1304,7 +1317,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     // ---------------------------------------------------------------- softmax
     const int X = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;  // row of the Q tile, tensor-memory lane
-    const int G = a.Hq / Hkv, TQ = 128 / G;
+    const int gs = a.g_shift, G = 1 << gs, TQ = 128 >> gs;
     const uint32_t tS = tmem + 256 * X + ((uint32_t)(quad * 32) << 16), tO = tS + 128;
     // fp16 probabilities: the running maximum is kept 7 below the scores', so that P <= 2^15
     constexpr float kShift = FP8 ? 7.f : 0.f;
@@ -1314,58 +1327,75 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     ChunkMeta meta = {};
     for (ChunkWalk w(a, start, units); w.valid(); w.next(), ++it) {
       const int qt = w.pair ? X : 0, tile_t0 = w.t0 + qt * TQ;
-      const int n_rows = min(TQ, w.n_q - tile_t0) * G;
+      const int n_rows = min(TQ, w.n_q - tile_t0) << gs;
       const bool valid = r < n_rows;
       const bool warp_valid = quad * 32 < n_rows;
-      const int tok = w.q0 + tile_t0 + r / G, head = w.g * G + r % G;
-      const int qpos = valid ? w.ctx + tile_t0 + r / G : w.n_keys - 1;
+      const int qpos = valid ? w.ctx + tile_t0 + (r >> gs) : w.n_keys - 1;
       q_loads0 += w.loads_q(0);
       float factor = kScaleLog2;
       if (w.loads_q(X)) {
-        // this thread's row of Q tile X into shared memory, 128-byte swizzle (zeros behind the last)
-        uint8_t* dst = smem + X * C::kQTile + r * 128;
+        // the warp's 32 rows of Q tile X into shared memory, 128-byte swizzle (zeros behind the
+        // last): 16 lanes a row, so that a load instruction takes two whole rows (a row a thread
+        // would be 32 separate lines an instruction, 3.6 us a tile)
+        const int d8 = lane & 15;  // dims [8 d8, 8 d8 + 8)
         uint4 v[16];
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)tok * a.ldq + (long long)head * kD);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if (!FP8) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * kTile8 + (((i & 7) ^ (r & 7)) << 4)) = v[i];
-        } else {
-          // q = 2^e (t1 + t2), the largest value scaled into [128, 256)
-          uint32_t mx = 0;
+        for (int i = 0; i < 16; ++i) {
+          const int row = quad * 32 + 2 * i + (lane >> 4);
+          v[i] = ld_or_zero(a.q + (long long)(w.q0 + tile_t0 + (row >> gs)) * a.ldq +
+                                ((long long)(w.g * G + (row & (G - 1))) * kD + 8 * d8),
+                            row < n_rows);
+        }
+        float down = 1.f;  // e4m3: of row 2 d8 + (lane >> 4), the row that the exchange below leaves here
+        if (FP8) {
+          // q = 2^e (t1 + t2), the row's largest value scaled into [128, 256): t1 the leading 4
+          // significant bits, t2 the other 4. Largest values by halving exchanges over the 16
+          // lanes of a row: 15 shuffles for 16 rows.
+          uint32_t mx[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx = max(mx, max(x[j] & 0x7fffu, (x[j] >> 16) & 0x7fffu));
+            const uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                         __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+            mx[i] = max(m2 & 0xffffu, m2 >> 16);
           }
-          const int ex = (int)(mx >> 7);
-          const int e = min(max(ex - 127 - 7, -119), 119);
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          factor = ex == 255 ? __uint_as_float(0x7fc00000u)
-                             : kScaleLog2 * a.kv.k_scale[w.g] * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // 16 values
+          for (int half = 8; half >= 1; half >>= 1) {
+            const bool upper = (lane & half) != 0;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+              const uint32_t send = upper ? mx[i] : mx[i + half], keep = upper ? mx[i + half] : mx[i];
+              mx[i] = max(keep, __shfl_xor_sync(0xffffffffu, send, half));
+            }
+          }
+          const int ex = (int)(mx[0] >> 7);
+          const int e = min(max(ex - 127 - 7, -119), 119);
+          down = __uint_as_float((uint32_t)(127 - e) << 23);
+          const float up = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23);
+          factor = kScaleLog2 * a.kv.k_scale[w.g] * __shfl_sync(0xffffffffu, up, (lane & 1) * 16 + (lane >> 1));
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = quad * 32 + 2 * i + (lane >> 4);
+          uint8_t* dst = smem + X * C::kQTile + row * 128;
+          if (!FP8) {
+            *reinterpret_cast<uint4*>(dst + (d8 >> 3) * kTile8 + (((d8 & 7) ^ (row & 7)) << 4)) = v[i];
+          } else {
+            const float dn = __shfl_sync(0xffffffffu, down, (lane & 16) + i);
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             uint32_t t1[4], t2[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint4& vv = v[2 * i + (j >> 1)];
-              const uint32_t x0 = j & 1 ? vv.z : vv.x, x1 = j & 1 ? vv.w : vv.y;
-              const float f0 = bf16_lo(x0) * down, f1 = bf16_hi(x0) * down, f2 = bf16_lo(x1) * down,
-                          f3 = bf16_hi(x1) * down;
-              const uint16_t p0 = pack_e4m3x2(f0, f1), p1 = pack_e4m3x2(f2, f3);
-              const float2 b0 = e4m3x2_to_f32x2(p0), b1 = e4m3x2_to_f32x2(p1);
-              t1[j] = p0 | ((uint32_t)p1 << 16);
-              t2[j] = pack_e4m3x2(f0 - b0.x, f1 - b0.y) | ((uint32_t)pack_e4m3x2(f2 - b1.x, f3 - b1.y) << 16);
+              const uint32_t h = x[j] & 0xfff0fff0u;
+              const float h0 = bf16_lo(h) * dn, h1 = bf16_hi(h) * dn;
+              t1[j] = pack_e4m3x2(h0, h1);
+              t2[j] = pack_e4m3x2(bf16_lo(x[j]) * dn - h0, bf16_hi(x[j]) * dn - h1);
             }
-            uint8_t* d = dst + ((i ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-            *reinterpret_cast<uint4*>(d + kTile8) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+            uint8_t* d = dst + (((d8 >> 1) ^ (row & 7)) << 4) + (d8 & 1) * 8;
+            *reinterpret_cast<uint2*>(d) = make_uint2(t1[0] | (t1[1] << 16), t1[2] | (t1[3] << 16));
+            *reinterpret_cast<uint2*>(d + kTile8) = make_uint2(t2[0] | (t2[1] << 16), t2[2] | (t2[3] << 16));
           }
-          if (!w.pair) ml[256 + r] = factor;  // for warpgroup 1
         }
+        if (FP8 && !w.pair) ml[256 + r] = factor;  // for warpgroup 1
         fence_proxy_async_smem();
         arrive_warp(&q_full[X], lane);
       } else if (FP8 && w.any(X)) {
@@ -1521,8 +1551,11 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         const bool whole = w.k0 == 0 && w.k1 >= nk;
         const float vs = FP8 ? a.kv.v_scale[w.g] : 1.f;
         const float mul = whole ? vs / l_run : 1.f;
-        uint16_t* dst = a.out + (long long)tok * a.ldo + (long long)head * kD;
         float* part = a.part + ((long long)(blockIdx.x * 2 + (w.k0 > 0 ? 0 : 1)) * 2 + X) * kChunkPart;
+        // finished rows go through the Q tile (whose scores are all done): a row a thread into
+        // shared memory, two whole rows an instruction from there
+        uint8_t* stage = smem + X * C::kQTile;
+        const bool f16 = a.o_f16 != 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -1536,8 +1569,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
             for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + (w1 != 0.f ? __uint_as_float(o1[i]) * w1 : 0.f));
           }
-          if (valid && whole) {
-            const bool f16 = a.o_f16 != 0;
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 q;
@@ -1545,11 +1577,26 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
               q.y = pack_op_x2(f16, __uint_as_float(o[8 * i + 2]) * mul, __uint_as_float(o[8 * i + 3]) * mul);
               q.z = pack_op_x2(f16, __uint_as_float(o[8 * i + 4]) * mul, __uint_as_float(o[8 * i + 5]) * mul);
               q.w = pack_op_x2(f16, __uint_as_float(o[8 * i + 6]) * mul, __uint_as_float(o[8 * i + 7]) * mul);
-              *reinterpret_cast<uint4*>(dst + c * 32 + i * 8) = q;
+              *reinterpret_cast<uint4*>(stage + r * 256 + (((c * 4 + i) ^ (r & 15)) << 4)) = q;
             }
           } else if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) __stcg(part + (c * 32 + i) * 128 + r, __uint_as_float(o[i]));
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4*>(part + (c * 32 + i) * 128 + r * 4),
+                     make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                 __uint_as_float(o[i + 3])));
+          }
+        }
+        __syncwarp();
+        if (whole) {
+          const int d8 = lane & 15;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = quad * 32 + 2 * i + (lane >> 4);
+            if (row < n_rows)
+              *reinterpret_cast<uint4*>(a.out + (long long)(w.q0 + tile_t0 + (row >> gs)) * a.ldo +
+                                        ((long long)(w.g * G + (row & (G - 1))) * kD + 8 * d8)) =
+                  *reinterpret_cast<const uint4*>(stage + row * 256 + ((d8 ^ (row & 15)) << 4));
           }
           __syncwarp();
         }
@@ -1610,14 +1657,17 @@ __global__ void __launch_bounds__(128) paged_chunk_join_kernel(const PagedAttn a
     const float w = mi == -INFINITY ? 0.f : exp2f(mi - M);
     L += li * w;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float v = __ldcg(p + (d0 + j) * 128 + r);
-      o[j] += w != 0.f ? v * w : 0.f;
+    for (int j = 0; j < 16; j += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + (d0 + j) * 128 + r * 4));
+      o[j] += w != 0.f ? v.x * w : 0.f;
+      o[j + 1] += w != 0.f ? v.y * w : 0.f;
+      o[j + 2] += w != 0.f ? v.z * w : 0.f;
+      o[j + 3] += w != 0.f ? v.w * w : 0.f;
     }
   }
-  const int G = a.Hq / a.kv.Hkv;
+  const int gs = a.g_shift, G = 1 << gs;
   const float mul = (a.kv.fp8 ? a.kv.v_scale[m.g] : 1.f) / L;
-  uint16_t* dst = a.out + (long long)(m.tok + r / G) * a.ldo + (long long)(m.g * G + r % G) * kD + d0;
+  uint16_t* dst = a.out + (long long)(m.tok + (r >> gs)) * a.ldo + (long long)(m.g * G + (r & (G - 1))) * kD + d0;
   const bool f16 = a.o_f16 != 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -1741,6 +1791,8 @@ int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int m
   a.pb = pb;
   a.kv = kv;
   a.n_tokens = n_tokens; a.max_q = max_q; a.Hq = Hq; a.o_f16 = o_f16 ? 1 : 0;
+  a.g_shift = 0;
+  while ((kv.Hkv << a.g_shift) < Hq) ++a.g_shift;
   a.q = q; a.ldq = ldq;
   a.out = out; a.ldo = ldo;
   a.plan = reinterpret_cast<long long*>(base + off.plan);
