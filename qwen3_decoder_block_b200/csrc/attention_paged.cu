@@ -1018,6 +1018,11 @@ struct ChunkWalk {
   __device__ int step() const { return pair ? 1 : 2; }
   __device__ int end(int X) const { return pair && X == 0 ? min(k1, nk0) : k1; }
   __device__ bool any(int X) const { return first(X) < end(X); }
+  // 64-key halves of tile k that warpgroup X needs (the last tile's second half may lie behind every row)
+  __device__ int halves(int X, int k) const {
+    const int keys = pair && X == 0 ? ctx + t0 + TQ : n_keys;
+    return k * kTileK + 64 < keys ? 2 : 1;
+  }
   __device__ bool loads_q(int X) const { return pair ? any(X) : X == 0; }
 };
 
@@ -1055,8 +1060,11 @@ struct ChunkCfg {
   static constexpr uint32_t kSmem = kOffBar + 40 * 8 + 16 + 1024;
 };
 
-// Tensor memory (512 columns): warpgroup X owns columns [256 X, 256 X + 256): S_X = [256 X, 256 X + 128)
-// (fp32 scores; columns [64, 128) are reused for the 16-bit probabilities), O_X = the other 128.
+// Tensor memory (512 columns): warpgroup X owns columns [256 X, 256 X + 256): two buffers of 64 for the
+// fp32 scores of half a KV tile, each reused for its 16-bit probabilities, and O_X in the other 128. While
+// the softmax works on one buffer, the tensor core does P.V from the other and the scores that
+// replace it: with whole tiles in one buffer that round trip was part of every tile (4930 clocks
+// a tile of a pair).
 template <bool FP8>
 __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     attn_paged_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -1074,16 +1082,14 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
   uint64_t* v_empty = bars + 12;    // [NV] two arrivals a tile
   uint64_t* raw_full = bars + 14;   // [2] e4m3 V tile loaded
   uint64_t* raw_empty = bars + 16;  // [2]
-  uint64_t* s_full = bars + 18;     // [2] scores of X ready
-  uint64_t* s_read = bars + 20;     // [2] scores of X in registers
-  uint64_t* p_full = bars + 22;     // [2] P_X written (and O_X rescaled)
-  uint64_t* pv_done = bars + 24;    // [2] P.V of X's tile complete
-  uint64_t* drain = bars + 26;      // [2] an issuer's MMAs complete
+  uint64_t* s_full = bars + 18;     // [X][buffer] scores of a half tile ready
+  uint64_t* p_full = bars + 22;     // [X][buffer] P written (and O_X rescaled)
+  uint64_t* pv_done = bars + 26;    // [X][buffer] P.V of the half tile complete
+  uint64_t* drain = bars + 30;      // [2] an issuer's MMAs complete
   // both warpgroups and both issuers are through with an item: nobody gets more than one item
   // ahead, so that no wait can take an older phase of a barrier for the one it means
-  uint64_t* item_done = bars + 28;
-  uint64_t* turn = bars + 29;       // [2] pairs: warpgroup X may start its exponentials
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
+  uint64_t* item_done = bars + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* ml = reinterpret_cast<float*>(smem + C::kOffML);
   int* err = a.err;
@@ -1096,12 +1102,12 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
       mbar_init(&v_empty[i], 2);
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
+      mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_read[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&drain[i], 1);
-      mbar_init(&turn[i], 4);
     }
     for (int i = 0; i < NK; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
     mbar_init(item_done, 8 + 2);
@@ -1244,65 +1250,65 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         q_loads[1] += w.loads_q(1);
         // arrivals this issuer owes a stage: its own, and the other's where that one skips the tile
         auto arrivals = [&](int k) { return !w.pair || (X == 1 && k >= w.nk0) ? 2 : 1; };
-        // S_X of tile k in two N = 64 halves: keys [0, 64) may go to columns [0, 64) as soon as
-        // the softmax has read the previous scores; columns [64, 128) hold P until its P.V is
-        // complete
-        auto issue_s_half = [&](int k, int h) -> bool {
+        // scores of half h of tile k, the X's nth half tile, into buffer n & 1
+        auto issue_s = [&](int k, int h, int n) -> bool {
           const int c = c0 + (k - w.k0), st = c % NK;
           if (*s_abort || !mbar_wait(&k_full[st], (uint32_t)((c / NK) & 1), err)) return false;
           tc_fence_after();
           const uint32_t sk = smem_u32(smem + C::kOffK + st * C::kKTile) + h * 64 * 128;
+          const uint32_t d = tmem + 256 * X + 64 * (n & 1);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t ad = sdesc_kmajor_sw128(qa + (kk >> 2) * kTile8) + 2 * (kk & 3);
             if (FP8)  // both terms of q against the same K
-              mma_e4m3_ss(tmem + 256 * X + 64 * h, ad, sdesc_kmajor_sw128(sk) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
+              mma_e4m3_ss(d, ad, sdesc_kmajor_sw128(sk) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
             else
-              mma_bf16_ss(tmem + 256 * X + 64 * h, ad, sdesc_kmajor_sw128(sk + (kk >> 2) * kTile8) + 2 * (kk & 3),
-                          idesc_s, kk ? 1u : 0u);
+              mma_bf16_ss(d, ad, sdesc_kmajor_sw128(sk + (kk >> 2) * kTile8) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
           }
-          if (h == 1) {
-            mma_commit(&s_full[X]);
+          mma_commit(&s_full[2 * X + (n & 1)]);
+          if (h + 1 == w.halves(X, k))
             for (int i = arrivals(k); i > 0; --i) mma_commit(&k_empty[st]);
-          }
           return true;
         };
         if (kb < ke) {
+          // the item's first two half tiles: both buffers are free since the last item ended
           ok = !*s_abort && mbar_wait(&q_full[qt], (uint32_t)((q_loads[qt] - 1) & 1), err);
-          // the scores of the previous item are read and its P.V complete
-          if (ok && u > 0)
-            ok = mbar_wait(&s_read[X], (uint32_t)((u - 1) & 1), err) &&
-                 mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
           if (ok) {
             tc_fence_after();
-            ok = issue_s_half(kb, 0) && issue_s_half(kb, 1);
+            ok = issue_s(kb, 0, u);
+            if (ok && w.halves(X, kb) == 2) ok = issue_s(kb, 1, u + 1);
+            else if (ok && kb + step < ke) ok = issue_s(kb + step, 0, u + 1);
           }
         }
-        for (int k = kb; k < ke && ok; k += step, ++u) {
-          const bool more = k + step < ke;
-          const uint32_t par = (uint32_t)(u & 1);
-          if (more) {
-            if (*s_abort || !mbar_wait(&s_read[X], par, err)) { ok = false; break; }
+        for (int k = kb; k < ke && ok; k += step) {
+          const int nh = w.halves(X, k), c = c0 + (k - w.k0), st = c % NV;
+          for (int h = 0; h < nh; ++h, ++u) {
+            const int bi = 2 * X + (u & 1);
+            const uint32_t par = (uint32_t)((u >> 1) & 1);
+            if (*s_abort || !mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err) ||
+                !mbar_wait(&p_full[bi], par, err)) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            if (!issue_s_half(k + step, 0)) { ok = false; break; }
-          }
-          const int c = c0 + (k - w.k0), st = c % NV;
-          if (*s_abort || !mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err) || !mbar_wait(&p_full[X], par, err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sv = smem_u32(smem + C::kOffV + st * C::kVTile);
+            const uint32_t sv = smem_u32(smem + C::kOffV + st * C::kVTile) + h * 64 * 128;
+            const uint32_t tp = tmem + 256 * X + 64 * (u & 1);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + 256 * X + 128, tmem + 256 * X + 64 + kk * 8,
-                        sdesc_mnmajor_sw128(sv + kk * 16 * 128, kTile8, 1024), idesc_o, (k != kb || kk) ? 1u : 0u);
-          mma_commit(&pv_done[X]);
-          for (int i = arrivals(k); i > 0; --i) mma_commit(&v_empty[st]);
-          if (more) {
-            if (*s_abort || !mbar_wait(&pv_done[X], par, err)) { ok = false; break; }
-            tc_fence_after();
-            if (!issue_s_half(k + step, 1)) { ok = false; break; }
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(tmem + 256 * X + 128, tp + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, kTile8, 1024),
+                          idesc_o, (k != kb || h || kk) ? 1u : 0u);
+            mma_commit(&pv_done[bi]);
+            if (h + 1 == nh)
+              for (int i = arrivals(k); i > 0; --i) mma_commit(&v_empty[st]);
+            // the half tile after the next one takes this one's buffer: P must have been read
+            int k2 = k, h2 = h + 2;
+            if (h2 >= nh) { k2 += step; h2 -= nh; }
+            if (k2 < ke && h2 >= w.halves(X, k2)) { h2 -= w.halves(X, k2); k2 += step; }
+            if (k2 < ke) {
+              if (*s_abort || !mbar_wait(&pv_done[bi], par, err)) { ok = false; break; }
+              tc_fence_after();
+              if (!issue_s(k2, h2, u + 2)) { ok = false; break; }
+            }
           }
         }
         c0 += w.k1 - w.k0;
@@ -1322,7 +1328,6 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     // fp16 probabilities: the running maximum is kept 7 below the scores', so that P <= 2^15
     constexpr float kShift = FP8 ? 7.f : 0.f;
     int c0 = 0, u = 0, q_loads0 = 0, it = 0;
-    int turns = 0;  // the other warpgroup's tiles of pairs so far
     bool ok = true;
     ChunkMeta meta = {};
     for (ChunkWalk w(a, start, units); w.valid(); w.next(), ++it) {
@@ -1406,120 +1411,103 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
       }
       float m_run = -INFINITY, l_run = 0.f;
       const int kb = w.first(X), ke = w.end(X), step = w.step();
-      for (int k = kb; k < ke; k += step, ++u) {
-        const uint32_t par = (uint32_t)(u & 1);
-        ok = ok && !*s_abort && mbar_wait(&s_full[X], par, err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
-          tc_fence_before();
-          arrive_warp(&s_read[X], lane);
-          if (w.pair) arrive_warp(&turn[X ^ 1], lane);
-          if (!FP8 && ok && k * kTileK + kTileK > w.n_keys) {
+      for (int k = kb; k < ke; k += step) {
+        const int nh = w.halves(X, k);
+        for (int h = 0; h < nh; ++h, ++u) {
+          const int bi = 2 * X + (u & 1);
+          const uint32_t tSb = tS + 64 * (u & 1);
+          const int kv0 = k * kTileK + 64 * h;
+          ok = ok && !*s_abort && mbar_wait(&s_full[bi], (uint32_t)((u >> 1) & 1), err);
+          ok = __all_sync(0xffffffffu, ok);
+          // bf16 V: zero the tile's rows past the last key (0 * NaN would poison O); both
+          // warpgroups of a pair do so before they release their P (zeros over zeros)
+          if (!FP8 && h == 0 && kv0 + kTileK > w.n_keys) {
             const int c = c0 + (k - w.k0), st = c % NV;
-            ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
-            if (ok && k * kTileK + r >= w.n_keys) {
+            ok = __all_sync(0xffffffffu, ok && !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
+            if (ok && kv0 + r >= w.n_keys) {
               uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
 #pragma unroll
               for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
-          arrive_warp(&p_full[X], lane);
-          continue;
-        }
-        tc_fence_after();
-        const int kv0 = k * kTileK;
-        const bool need_mask = __any_sync(0xffffffffu, kv0 + kTileK - 1 > qpos);
-        // the whole 128-column score row of this thread in one tensor-memory round trip
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(v[c]);
-        tc_fence_before();
-        arrive_warp(&s_read[X], lane);  // columns [0, 64) of S_X may now take the next tile's scores
-        if (need_mask) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (kv0 + c * 32 + i > qpos) v[c][i] = __float_as_uint(-INFINITY);
-        }
-        float mc[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mc[c] = __uint_as_float(v[c][0]);
-#pragma unroll
-          for (int i = 1; i < 31; i += 2) mc[c] = fmax3(mc[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-          mc[c] = fmaxf(mc[c], __uint_as_float(v[c][31]));
-        }
-        const float mxs = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * factor - kShift;
-        float alpha = 1.f;
-        if (mxs > m_run + kRescaleThreshold || m_run == -INFINITY) {
-          alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mxs);
-          m_run = mxs;
-        }
-        // p = 2^(s factor - m); a row that has seen no key yet (its causal limit lies before
-        // this tile) keeps m = -inf and p = 2^-inf = 0
-        const float neg = m_run == -INFINITY ? 0.f : -m_run;
-        const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
-        const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
-        uint64_t acc2[2] = {0ull, 0ull};
-        // The warpgroups of a pair take turns on the exponentials (the special-function unit
-        // bounds the softmax), so that each turn overlaps the tensor core's work on the other
-        // Q tile: tile k of 0 goes after tile k - 1 of 1, tile k of 1 after tile k of 0 (if 0 has it).
-        if (w.pair && (X == 0 ? k > kb : k < w.end(0))) {
-          const int n = turns + (k - kb) - (X == 0 ? 1 : 0);
-          ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&turn[X], (uint32_t)(n & 1), err));
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const uint64_t e = f2_fma(f2_pack(v[c][i], v[c][i + 1]), scale2, neg2);
-            const float p0 = ex2_approx(f2_lo(e));
-            const float p1 = ex2_approx(f2_hi(e));
-            acc2[(i >> 1) & 1] = f2_add(acc2[(i >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-            v[c][i >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
+            tc_fence_before();
+            arrive_warp(&p_full[bi], lane);
+            continue;
           }
-          tmem_st16(tS + 64 + c * 16, v[c]);
-        }
-        if (w.pair) arrive_warp(&turn[X ^ 1], lane);
-        const uint64_t acc = f2_add(acc2[0], acc2[1]);
-        l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
-        // O_X is stable here: the second half of S_X was issued only after the previous P.V completed
-        if (k > kb && __any_sync(0xffffffffu, alpha != 1.f)) {
+          tc_fence_after();
+          const bool need_mask = __any_sync(0xffffffffu, kv0 + 63 > qpos);
+          uint32_t v[2][32];
+          tmem_ld32(tSb, v[0]);
+          tmem_ld32(tSb + 32, v[1]);
+          tmem_wait_ld_regs(v[0]);
+          tmem_wait_ld_regs(v[1]);
+          if (need_mask) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (kv0 + c * 32 + i > qpos) v[c][i] = __float_as_uint(-INFINITY);
+          }
+          float mc[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_wait_ld_regs(o);
+            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
+            mc[c] = __uint_as_float(x[0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tO + c * 32, o);
+            for (int i = 1; i < 15; i += 2) mc[c] = fmax3(mc[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            mc[c] = fmaxf(mc[c], __uint_as_float(x[15]));
           }
-        }
-        // bf16 V: zero the rows past the last key (0 * NaN would poison O); both warpgroups
-        // of a pair do so before they release their P (the second writes zeros over zeros)
-        if (!FP8 && kv0 + kTileK > w.n_keys) {
-          const int c = c0 + (k - w.k0), st = c % NV;
-          ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
-          if (ok && kv0 + r >= w.n_keys) {
-            uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
+          const float mxs = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * factor - kShift;
+          float alpha = 1.f;
+          if (mxs > m_run + kRescaleThreshold || m_run == -INFINITY) {
+            alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mxs);
+            m_run = mxs;
+          }
+          // p = 2^(s factor - m); a row that has seen no key yet (its causal limit lies before
+          // this half tile) keeps m = -inf and p = 2^-inf = 0
+          const float neg = m_run == -INFINITY ? 0.f : -m_run;
+          const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
+          const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
+          uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const uint64_t e = f2_fma(f2_pack(v[c][i], v[c][i + 1]), scale2, neg2);
+              const float p0 = ex2_approx(f2_lo(e));
+              const float p1 = ex2_approx(f2_hi(e));
+              acc2[(i >> 1) & 1] = f2_add(acc2[(i >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+              v[c][i >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tSb + c * 16, v[c]);
           }
-          fence_proxy_async_smem();
+          const uint64_t acc = f2_add(acc2[0], acc2[1]);
+          l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
+          if ((k > kb || h) && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O_X is stable once the previous half tile's P.V is complete
+            ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&pv_done[bi ^ 1], (uint32_t)(((u - 1) >> 1) & 1), err));
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          arrive_warp(&p_full[bi], lane);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_warp(&p_full[X], lane);
       }
       c0 += w.k1 - w.k0;
-      if (w.pair) turns += max(w.end(X ^ 1) - w.first(X ^ 1), 0);
       const bool any = kb < ke;
       if (any) {
-        ok = ok && !*s_abort && mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
+        ok = ok && !*s_abort && mbar_wait(&pv_done[2 * X + ((u - 1) & 1)], (uint32_t)(((u - 1) >> 1) & 1), err);
         ok = __all_sync(0xffffffffu, ok);
       }
       // a single item's other half: warpgroup 1 leaves m, l in shared memory and O_1 in place
