@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           mbar_wait(&q_full[i & 1], (uint32_t)((i >> 1) & 1), err);
     }
   } else if (warp == SW + 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ S issuer: S = K q
       constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 0, 0) : idesc_bf16_f32(128, NC, 0, 0);
       int tc = 0, st = 0, rows_seen = 0;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       mbar_wait(&drain[0], 0, err);
     }
   } else if (warp == SW + 2) {
-    if (lane == 0) {
+    if (elect_one()) {
       // -------------------------------------------- P.V issuer: O^T += V^T P^T
       constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 1, 0) : idesc_bf16_f32(128, NC, 1, 0);
       int tc = 0, st = 0;
@@ -1039,6 +1039,10 @@ __device__ __forceinline__ uint4 ld_or_zero(const void* p, bool there) {
   return v;
 }
 
+// A shared-memory matrix descriptor moved by `bytes` (addresses stay below 2^18, so the 14-bit
+// field of 16-byte units does not overflow).
+__device__ __forceinline__ uint64_t desc_step(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
 template <bool FP8>
 struct ChunkCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;  // softmax 0, 1; control (K, MMA 0, MMA 1, V); V widening
@@ -1231,11 +1235,16 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         // let the copies still in flight land before the CTA exits
         for (int i = done > ns ? done - ns : 0; i < done; ++i) mbar_wait(&full[i % ns], (uint32_t)((i / ns) & 1), err);
       }
-    } else if (lane == 0) {
+    } else if (elect_one()) {
       // --------------------------------------------------- MMA issuers, one per warpgroup X
       const int X = warp - 9;
       constexpr uint32_t idesc_s = FP8 ? idesc_e4m3_f32(128, 64, 0, 0) : idesc_bf16_f32(128, 64, 0, 0);
       constexpr uint32_t idesc_o = FP8 ? idesc_f16_f32(128, kD, 0, 1) : idesc_bf16_f32(128, kD, 0, 1);
+      // One thread issues every product of X, so its instructions count: elected rather than
+      // picked by lane number (eight products take 141 clocks to issue, not 510), descriptors
+      // built once and stepped by constants.
+      const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
+      const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(smem + C::kOffV), kTile8, 1024);
       int c0 = 0, u = 0, q_loads[2] = {0, 0}, it = 0;
       bool ok = true;
       for (ChunkWalk w(a, start, units); w.valid() && ok; w.next(), ++it) {
@@ -1245,7 +1254,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         }
         const int kb = w.first(X), ke = w.end(X), step = w.step();
         const int qt = w.pair ? X : 0;  // the Q tile
-        const uint32_t qa = smem_u32(smem) + qt * C::kQTile;
+        const uint64_t qd = desc_step(sdesc_kmajor_sw128(smem_u32(smem)), qt * C::kQTile);
         q_loads[0] += w.loads_q(0);
         q_loads[1] += w.loads_q(1);
         // arrivals this issuer owes a stage: its own, and the other's where that one skips the tile
@@ -1255,15 +1264,15 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
           const int c = c0 + (k - w.k0), st = c % NK;
           if (*s_abort || !mbar_wait(&k_full[st], (uint32_t)((c / NK) & 1), err)) return false;
           tc_fence_after();
-          const uint32_t sk = smem_u32(smem + C::kOffK + st * C::kKTile) + h * 64 * 128;
+          const uint64_t kd = desc_step(k_desc, st * C::kKTile + h * 64 * 128);
           const uint32_t d = tmem + 256 * X + 64 * (n & 1);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t ad = sdesc_kmajor_sw128(qa + (kk >> 2) * kTile8) + 2 * (kk & 3);
+            const uint64_t ad = desc_step(qd, (kk >> 2) * kTile8 + 32 * (kk & 3));
             if (FP8)  // both terms of q against the same K
-              mma_e4m3_ss(d, ad, sdesc_kmajor_sw128(sk) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
+              mma_e4m3_ss(d, ad, desc_step(kd, 32 * (kk & 3)), idesc_s, kk ? 1u : 0u);
             else
-              mma_bf16_ss(d, ad, sdesc_kmajor_sw128(sk + (kk >> 2) * kTile8) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
+              mma_bf16_ss(d, ad, desc_step(kd, (kk >> 2) * kTile8 + 32 * (kk & 3)), idesc_s, kk ? 1u : 0u);
           }
           mma_commit(&s_full[2 * X + (n & 1)]);
           if (h + 1 == w.halves(X, k))
@@ -1291,12 +1300,11 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t sv = smem_u32(smem + C::kOffV + st * C::kVTile) + h * 64 * 128;
+            const uint64_t vd = desc_step(v_desc, st * C::kVTile + h * 64 * 128);
             const uint32_t tp = tmem + 256 * X + 64 * (u & 1);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + 256 * X + 128, tp + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, kTile8, 1024),
-                          idesc_o, (k != kb || h || kk) ? 1u : 0u);
+              mma_bf16_ts(tmem + 256 * X + 128, tp + kk * 8, desc_step(vd, kk * 16 * 128), idesc_o, (k != kb || h || kk) ? 1u : 0u);
             mma_commit(&pv_done[bi]);
             if (h + 1 == nh)
               for (int i = arrivals(k); i > 0; --i) mma_commit(&v_empty[st]);

@@ -45,8 +45,8 @@ template <int N>
 __device__ __forceinline__ void regs_decrease() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // One lane of a converged warp, chosen by the hardware: the compiler then knows that the code
-// under it runs in a single thread (tensor copies take uniform operands; under a plain lane
-// test they are issued from a loop over the lanes).
+// under it runs in a single thread (tensor copies and tensor-core products take uniform
+// operands; under a plain lane test each is issued from a loop over the lanes).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
