@@ -1257,13 +1257,15 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         const uint64_t qd = desc_step(sdesc_kmajor_sw128(smem_u32(smem)), qt * C::kQTile);
         q_loads[0] += w.loads_q(0);
         q_loads[1] += w.loads_q(1);
-        // arrivals this issuer owes a stage: its own, and the other's where that one skips the tile
-        auto arrivals = [&](int k) { return !w.pair || (X == 1 && k >= w.nk0) ? 2 : 1; };
-        // scores of half h of tile k, the X's nth half tile, into buffer n & 1
-        auto issue_s = [&](int k, int h, int n) -> bool {
-          const int c = c0 + (k - w.k0), st = c % NK;
-          if (*s_abort || !mbar_wait(&k_full[st], (uint32_t)((c / NK) & 1), err)) return false;
-          tc_fence_after();
+        // arrivals this issuer owes a stage of tile k: its own, and the other's where that one skips it
+        const int twice_from = w.pair ? (X == 1 ? w.nk0 : w.k1) : 0;
+        // scores of half h of tile k, X's nth half tile, into buffer n & 1
+        auto issue_s = [&](int k, int h, int n, bool last_half) -> bool {
+          const int c = c0 + (k - w.k0), st = c & (NK - 1);
+          if (h == 0) {
+            if (!mbar_wait(&k_full[st], (uint32_t)((c / NK) & 1), err)) return false;
+            tc_fence_after();
+          }
           const uint64_t kd = desc_step(k_desc, st * C::kKTile + h * 64 * 128);
           const uint32_t d = tmem + 256 * X + 64 * (n & 1);
 #pragma unroll
@@ -1275,49 +1277,52 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
               mma_bf16_ss(d, ad, desc_step(kd, (kk >> 2) * kTile8 + 32 * (kk & 3)), idesc_s, kk ? 1u : 0u);
           }
           mma_commit(&s_full[2 * X + (n & 1)]);
-          if (h + 1 == w.halves(X, k))
-            for (int i = arrivals(k); i > 0; --i) mma_commit(&k_empty[st]);
+          if (last_half) {
+            mma_commit(&k_empty[st]);
+            if (k >= twice_from) mma_commit(&k_empty[st]);
+          }
           return true;
         };
+        // P.V of half h of tile k, then the scores of half h of the next tile, which take its buffer
+        auto issue_half = [&](int k, int h, bool last_half, int next_halves) -> bool {
+          const int c = c0 + (k - w.k0), st = c & (NV - 1), bi = 2 * X + (u & 1);
+          const uint32_t par = (uint32_t)((u >> 1) & 1);
+          if (h == 0 && !mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err)) return false;
+          if (!mbar_wait(&p_full[bi], par, err)) return false;
+          tc_fence_after();
+          const uint64_t vd = desc_step(v_desc, st * C::kVTile + h * 64 * 128);
+          const uint32_t tp = tmem + 256 * X + 64 * (u & 1);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(tmem + 256 * X + 128, tp + kk * 8, desc_step(vd, kk * 16 * 128), idesc_o,
+                        (k != kb || h || kk) ? 1u : 0u);
+          mma_commit(&pv_done[bi]);
+          if (last_half) {
+            mma_commit(&v_empty[st]);
+            if (k >= twice_from) mma_commit(&v_empty[st]);
+          }
+          if (h < next_halves) {  // P must have been read
+            if (!mbar_wait(&pv_done[bi], par, err)) return false;
+            tc_fence_after();
+            if (!issue_s(k + step, h, u + 2, h + 1 == next_halves)) return false;
+          }
+          ++u;
+          return true;
+        };
+        // (only the item's last tile can have a single half)
         if (kb < ke) {
           // the item's first two half tiles: both buffers are free since the last item ended
+          const int nh = w.halves(X, kb);
           ok = !*s_abort && mbar_wait(&q_full[qt], (uint32_t)((q_loads[qt] - 1) & 1), err);
           if (ok) {
             tc_fence_after();
-            ok = issue_s(kb, 0, u);
-            if (ok && w.halves(X, kb) == 2) ok = issue_s(kb, 1, u + 1);
-            else if (ok && kb + step < ke) ok = issue_s(kb + step, 0, u + 1);
+            ok = issue_s(kb, 0, u, nh == 1) && (nh == 1 || issue_s(kb, 1, u + 1, true));
           }
         }
         for (int k = kb; k < ke && ok; k += step) {
-          const int nh = w.halves(X, k), c = c0 + (k - w.k0), st = c % NV;
-          for (int h = 0; h < nh; ++h, ++u) {
-            const int bi = 2 * X + (u & 1);
-            const uint32_t par = (uint32_t)((u >> 1) & 1);
-            if (*s_abort || !mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err) ||
-                !mbar_wait(&p_full[bi], par, err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t vd = desc_step(v_desc, st * C::kVTile + h * 64 * 128);
-            const uint32_t tp = tmem + 256 * X + 64 * (u & 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + 256 * X + 128, tp + kk * 8, desc_step(vd, kk * 16 * 128), idesc_o, (k != kb || h || kk) ? 1u : 0u);
-            mma_commit(&pv_done[bi]);
-            if (h + 1 == nh)
-              for (int i = arrivals(k); i > 0; --i) mma_commit(&v_empty[st]);
-            // the half tile after the next one takes this one's buffer: P must have been read
-            int k2 = k, h2 = h + 2;
-            if (h2 >= nh) { k2 += step; h2 -= nh; }
-            if (k2 < ke && h2 >= w.halves(X, k2)) { h2 -= w.halves(X, k2); k2 += step; }
-            if (k2 < ke) {
-              if (*s_abort || !mbar_wait(&pv_done[bi], par, err)) { ok = false; break; }
-              tc_fence_after();
-              if (!issue_s(k2, h2, u + 2)) { ok = false; break; }
-            }
-          }
+          const int nh = k + step < ke ? 2 : w.halves(X, k);
+          const int next_halves = k + step >= ke ? 0 : k + 2 * step < ke ? 2 : w.halves(X, k + step);
+          ok = !*s_abort && issue_half(k, 0, nh == 1, next_halves) && (nh == 1 || issue_half(k, 1, true, next_halves));
         }
         c0 += w.k1 - w.k0;
         mbar_arrive(item_done);
