@@ -27,8 +27,8 @@ constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte sw
 // it with one load).
 struct __align__(32) CtaStart {
   long long units;  // all units of the call
-  int b, g, j;      // sequence, KV group and tile of its first unit
-  int n_keys;       // keys of that row
+  int b, g, j;      // sequence, KV group and tile (decode form) or item (chunk form) of its first unit
+  int rest;         // decode form: keys of that row; chunk form: units of the item before the CTA's
 };
 
 struct ChunkMeta;
@@ -37,6 +37,8 @@ struct PagedAttn {
   PagedBatch pb;
   KvPages kv;
   int n_tokens, max_q, Hq, g_shift, o_f16;  // g_shift: log2 of the query heads per KV group
+  int min_q;         // chunk form: it takes the sequences with at least this many new tokens
+  int beside;        // chunk form: the decode form was launched just before, on its own part of the call
   const uint16_t* q;
   long long ldq;
   uint16_t* out;
@@ -54,7 +56,7 @@ struct PagedAttn {
 
 // ----------------------------------------------------------------------------
 // The work list. A sequence's work is counted in units (decode form: 128-key tiles of its
-// Hkv rows; chunk form: see chunk_units); plan[b] is the unit at which sequence b starts,
+// Hkv rows; chunk form: see ChunkSeq); plan[b] is the unit at which sequence b starts,
 // plan[B] all units, and CTA c of n takes units [c U / n, (c + 1) U / n): the same share
 // for every CTA whatever the lengths. A sequence that cannot be served holds no units and
 // is reported.
@@ -110,62 +112,127 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* wsum, 
 
 }  // namespace
 
-// Decode form, before the attention: block 0 writes the work list and clears the merge
-// counters; with e4m3 pages the other blocks split each query head (one per warp) into two
-// e4m3 terms, q = 2^e (t1 + t2 / 16): t1 keeps 4 significant bits, the remainder of a bf16
-// value (8 bits) fits the 4 of t2 exactly, down to 2^-14 of the head's largest value, below
-// which the error stays under 2^-23 of that value.
-__global__ void __launch_bounds__(kPlanThreads) paged_decode_prep_kernel(const PagedAttn a) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
+namespace {
+
+// Sum over p < P of the KV tiles of pair p, floor((ctx + min((p + 1) s, n_q) - 1) / 128) + 1, for
+// s = 2 TQ (a power of two, 16 to 256) and P <= ceil(n_q / s).
+__device__ __forceinline__ long long pair_tiles(int ctx, int n_q, int s, int P) {
+  if (P <= 0) return 0;
+  long long cut = 0;
+  if ((long long)P * s > n_q) {  // the last pair ends with the sequence
+    cut = ((long long)ctx + n_q - 1) / kTileK + 1;
+    --P;
+  }
+  const long long a = (long long)ctx + s - 1;
+  if (s >= kTileK) return cut + P * (a / kTileK + 1) + (long long)(s / kTileK) * P * (P - 1) / 2;
+  const int r = kTileK / s;  // floor((a + p s) / 128) = floor((floor(a / s) + p) / r)
+  auto F = [&](long long n) {
+    const long long m = n / r;
+    return r * (m * (m - 1) / 2) + m * (n - m * r);
+  };
+  return cut + P + F(a / s + P) - F(a / s);
+}
+struct ChunkSeq {
+  int n_q, ctx, s, pairs, odd;
+  long long head_units;  // of one KV head
+  __device__ ChunkSeq(int nq, int c, int g_shift) : n_q(nq), ctx(c), s(256 >> g_shift) {
+    const int tiles = (int)((((long long)nq << g_shift) + 127) >> 7);
+    pairs = tiles >> 1;
+    odd = tiles & 1;
+    head_units = 2 * pair_tiles(ctx, n_q, s, pairs) + (odd ? ((long long)ctx + n_q - 1) / kTileK + 1 : 0);
+  }
+};
+
+// One form's work list, CTA starts and cleared counters, by one block.
+template <bool CHUNK>
+__device__ void write_plan(const PagedAttn& a, long long* wsum, long long* plan_s) {
   const int B = a.pb.B, Hkv = a.kv.Hkv;
-  if (blockIdx.x == 0) {
-    __shared__ long long wsum[kPlanThreads / 32];
-    __shared__ long long plan_s[kPlanShared];
-    long long carry = 0;
-    for (int base = 0; base < B; base += kPlanThreads) {
-      const int b = base + (int)threadIdx.x;
-      long long v = 0, total;
-      int n_q, ctx;
-      if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err) && n_q > 0)
+  long long carry = 0;
+  for (int base = 0; base < B; base += kPlanThreads) {
+    const int b = base + (int)threadIdx.x;
+    long long v = 0, total;
+    int n_q, ctx;
+    if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err)) {
+      if (CHUNK) {
+        if (n_q >= a.min_q) v = Hkv * ChunkSeq(n_q, ctx, a.g_shift).head_units;
+      } else if (n_q == 1) {
         v = (long long)Hkv * ((ctx + kTileK) / kTileK);
-      const long long at = block_prefix(v, wsum, &total);
-      if (b < B) a.plan[b] = carry + at;
-      if (b < kPlanShared) plan_s[b] = carry + at;
-      carry += total;
+      }
     }
-    const long long* plan = B <= kPlanShared ? plan_s : a.plan;
-    if (threadIdx.x == 0) a.plan[B] = carry;
+    const long long at = block_prefix(v, wsum, &total);
+    if (b < B) a.plan[b] = carry + at;
+    if (b < kPlanShared) plan_s[b] = carry + at;
+    carry += total;
+  }
+  const long long* plan = B <= kPlanShared ? plan_s : a.plan;
+  if (threadIdx.x == 0) a.plan[B] = carry;
+  if (!CHUNK)
     for (int i = threadIdx.x; i < B * Hkv; i += kPlanThreads) a.counters[i] = 0;
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.n_cta; c += kPlanThreads) {
-      CtaStart s;
-      s.units = carry;
-      s.b = s.g = s.j = s.n_keys = 0;
-      const long long t = share(carry, c, a.n_cta);
-      if (t < share(carry, c + 1, a.n_cta)) {
-        int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) / 2;
-          if (plan[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        s.b = lo;
-        s.n_keys = a.pb.ctx_len[lo] + 1;
-        const int nt = (s.n_keys + kTileK - 1) / kTileK, at = (int)(t - plan[lo]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.n_cta; c += kPlanThreads) {
+    CtaStart s;
+    s.units = carry;
+    s.b = s.g = s.j = s.rest = 0;
+    const long long t = share(carry, c, a.n_cta);
+    if (t < share(carry, c + 1, a.n_cta)) {
+      int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (plan[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      s.b = lo;
+      if (!CHUNK) {
+        s.rest = a.pb.ctx_len[lo] + 1;
+        const int nt = (s.rest + kTileK - 1) / kTileK, at = (int)(t - plan[lo]);
         s.g = at / nt;
         s.j = at % nt;
+      } else {
+        const ChunkSeq q(a.pb.q_start[lo + 1] - a.pb.q_start[lo], a.pb.ctx_len[lo], a.g_shift);
+        long long r = t - plan[lo];
+        s.g = (int)(r / q.head_units);
+        r -= s.g * q.head_units;
+        lo = 0;
+        hi = q.pairs + q.odd - 1;  // the last item that starts at or before unit r of the head
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (2 * pair_tiles(q.ctx, q.n_q, q.s, mid) <= r) lo = mid; else hi = mid - 1;
+        }
+        s.j = lo;
+        s.rest = (int)(r - 2 * pair_tiles(q.ctx, q.n_q, q.s, lo));
       }
-      a.start[c] = s;
     }
+    a.start[c] = s;
+  }
+}
+
+}  // namespace
+
+// Before the attention: block 0 writes the decode form's work list, block 1 the chunk form's
+// (`forms`: bit 0 and 1). With e4m3 pages the other blocks split each query head of the decode
+// form (one per warp) into two e4m3 terms, q = 2^e (t1 + t2 / 16): t1 keeps 4 significant
+// bits, the remainder of a bf16 value (8 bits) fits the 4 of t2 exactly, down to 2^-14 of
+// the head's largest value, below which the error stays under 2^-22 of that value.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttn a, const PagedAttn chunk, int forms) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ long long wsum[kPlanThreads / 32];
+  __shared__ long long plan_s[kPlanShared];
+  if (blockIdx.x == 0) {
+    if (forms & 1) write_plan<false>(a, wsum, plan_s);
     return;
   }
-  const long long row = (long long)(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+  if (blockIdx.x == 1) {
+    if (forms & 2) write_plan<true>(chunk, wsum, plan_s);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int B = a.pb.B, Hkv = a.kv.Hkv;
+  const long long row = (long long)(blockIdx.x - 2) * (kPlanThreads / 32) + (threadIdx.x >> 5);
   const int b = (int)(row / a.Hq), h = (int)(row % a.Hq);
   if (b >= B) return;
   int n_q, ctx;
-  if (!paged_seq_ok(a, b, &n_q, &ctx, nullptr) || n_q == 0) return;
-  const int G = a.Hq / Hkv, g = h / G, j = h % G;
+  if (!paged_seq_ok(a, b, &n_q, &ctx, nullptr) || n_q != 1) return;
+  const int G = 1 << a.g_shift, g = h >> a.g_shift, j = h & (G - 1);
   const uint2 u = *reinterpret_cast<const uint2*>(a.q + a.pb.q_start[b] * a.ldq + (long long)h * kD + 4 * lane);
   float x[4] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
   const float mx = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
@@ -235,7 +302,7 @@ struct RowWalk {
   int B, Hkv, b, g, j0, j1, nt, n_keys;
   int left;  // the CTA's tiles from the current row on
   __device__ RowWalk(const PagedAttn& a, const CtaStart& s, int n_tiles)
-      : plan(a.plan), ctx_len(a.pb.ctx_len), B(a.pb.B), Hkv(a.kv.Hkv), b(s.b), g(s.g), j0(s.j), n_keys(s.n_keys),
+      : plan(a.plan), ctx_len(a.pb.ctx_len), B(a.pb.B), Hkv(a.kv.Hkv), b(s.b), g(s.g), j0(s.j), n_keys(s.rest),
         left(n_tiles) {
     set_row();
   }
@@ -876,88 +943,7 @@ struct ChunkMeta {
   int pad[2];
 };
 
-// Sum over p < P of the KV tiles of pair p, floor((ctx + min((p + 1) s, n_q) - 1) / 128) + 1, for
-// s = 2 TQ (a power of two, 16 to 256) and P <= ceil(n_q / s).
-__device__ __forceinline__ long long pair_tiles(int ctx, int n_q, int s, int P) {
-  if (P <= 0) return 0;
-  long long cut = 0;
-  if ((long long)P * s > n_q) {  // the last pair ends with the sequence
-    cut = ((long long)ctx + n_q - 1) / kTileK + 1;
-    --P;
-  }
-  const long long a = (long long)ctx + s - 1;
-  if (s >= kTileK) return cut + P * (a / kTileK + 1) + (long long)(s / kTileK) * P * (P - 1) / 2;
-  const int r = kTileK / s;  // floor((a + p s) / 128) = floor((floor(a / s) + p) / r)
-  auto F = [&](long long n) {
-    const long long m = n / r;
-    return r * (m * (m - 1) / 2) + m * (n - m * r);
-  };
-  return cut + P + F(a / s + P) - F(a / s);
-}
-struct ChunkSeq {
-  int n_q, ctx, s, pairs, odd;
-  long long head_units;  // of one KV head
-  __device__ ChunkSeq(int nq, int c, int g_shift) : n_q(nq), ctx(c), s(256 >> g_shift) {
-    const int tiles = (int)((((long long)nq << g_shift) + 127) >> 7);
-    pairs = tiles >> 1;
-    odd = tiles & 1;
-    head_units = 2 * pair_tiles(ctx, n_q, s, pairs) + (odd ? ((long long)ctx + n_q - 1) / kTileK + 1 : 0);
-  }
-};
-
 }  // namespace
-
-// Chunk form, before the attention: the work list and the CTA starts.
-__global__ void __launch_bounds__(kPlanThreads) paged_chunk_plan_kernel(const PagedAttn a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ long long wsum[kPlanThreads / 32];
-  __shared__ long long plan_s[kPlanShared];
-  const int B = a.pb.B, Hkv = a.kv.Hkv;
-  long long carry = 0;
-  for (int base = 0; base < B; base += kPlanThreads) {
-    const int b = base + (int)threadIdx.x;
-    long long v = 0, total;
-    int n_q, ctx;
-    if (b < B && paged_seq_ok(a, b, &n_q, &ctx, a.err) && n_q > 0) v = Hkv * ChunkSeq(n_q, ctx, a.g_shift).head_units;
-    const long long at = block_prefix(v, wsum, &total);
-    if (b < B) a.plan[b] = carry + at;
-    if (b < kPlanShared) plan_s[b] = carry + at;
-    carry += total;
-  }
-  const long long* plan = B <= kPlanShared ? plan_s : a.plan;
-  if (threadIdx.x == 0) a.plan[B] = carry;
-  __syncthreads();
-  for (int c = threadIdx.x; c < a.n_cta; c += kPlanThreads) {
-    CtaStart s;
-    s.units = carry;
-    s.b = s.g = s.j = 0;
-    s.n_keys = 0;
-    const long long t = share(carry, c, a.n_cta);
-    if (t < share(carry, c + 1, a.n_cta)) {
-      int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (plan[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      s.b = lo;
-      const ChunkSeq q(a.pb.q_start[lo + 1] - a.pb.q_start[lo], a.pb.ctx_len[lo], a.g_shift);
-      long long r = t - plan[lo];
-      s.g = (int)(r / q.head_units);
-      r -= s.g * q.head_units;
-      lo = 0;
-      hi = q.pairs;  // the last item that starts at or before unit r of the head
-      if (!q.odd) --hi;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (2 * pair_tiles(q.ctx, q.n_q, q.s, mid) <= r) lo = mid; else hi = mid - 1;
-      }
-      s.j = lo;
-      s.n_keys = (int)(r - 2 * pair_tiles(q.ctx, q.n_q, q.s, lo));  // units of the item before the CTA's
-    }
-    a.start[c] = s;
-  }
-}
 
 // Walk over the items that meet this CTA's units.
 struct ChunkWalk {
@@ -969,7 +955,7 @@ struct ChunkWalk {
   int t0, n_keys, nk0, n;  // first token; keys of the item; KV tiles of Q tile 0 (pair), of the item
   int k0, k1;              // the CTA's KV tiles
   __device__ ChunkWalk(const PagedAttn& a_, const CtaStart& s, long long units)
-      : a(a_), TQ(128 >> a_.g_shift), b(s.b), g(s.g), p(s.j), before(s.n_keys), left(units), k0(0), k1(0) {
+      : a(a_), TQ(128 >> a_.g_shift), b(s.b), g(s.g), p(s.j), before(s.rest), left(units), k0(0), k1(0) {
     if (left > 0) {
       set_seq();
       set_item();
@@ -1126,7 +1112,10 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
+  // After the decode form there is nothing to wait for: it waited for the plan before it let this
+  // kernel start, and the two write different rows. CTAs then start as decode CTAs exit; the
+  // wait at the end keeps this kernel from being complete before that one.
+  if (!a.beside) pdl_wait();
   pdl_trigger();
   const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
   const CtaStart start = a.start[blockIdx.x];
@@ -1631,6 +1620,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (a.beside) pdl_wait();
 }
 
 // Joins the partials of the Q tiles that span CTAs: blocks (c, X, 16 dims) with the tiles that
@@ -1686,25 +1676,33 @@ __global__ void __launch_bounds__(128) paged_chunk_join_kernel(const PagedAttn a
 // ----------------------------------------------------------------------------
 namespace {
 
-// Scratch of a call, in order: work list, CTA starts, merge counters (decode form) or what the CTAs
-// leave to join (chunk form), partials, e4m3 query terms and scales.
+// Scratch of one form, in order: work list, CTA starts, merge counters (decode form) or what the
+// CTAs leave to join (chunk form), partials, e4m3 query terms and scales (decode form).
 struct Scratch {
   size_t plan, start, counters, part, q8, q8_scale, bytes;
 };
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-Scratch scratch_of(int B, int Hq, int Hkv, int max_q) {
+Scratch scratch_of(bool chunk, int B, int Hq, int Hkv) {
   Scratch s;
-  const bool decode = max_q == 1;
   const size_t G = Hq / Hkv, rows = (size_t)B * Hkv;
   s.plan = 0;
   s.start = s.plan + up256(((size_t)B + 1) * sizeof(long long));
   s.counters = s.start + kMaxCtas * sizeof(CtaStart);
-  s.part = s.counters + up256(decode ? rows * sizeof(int) : 2 * kChunkCtas * sizeof(ChunkMeta));
-  s.q8 = s.part + up256((decode ? (rows + kMaxCtas) * G * kPartFloats : (size_t)4 * kChunkCtas * kChunkPart) * sizeof(float));
-  s.q8_scale = s.q8 + up256(decode ? (size_t)B * Hq * 2 * kD : 0);
-  s.bytes = s.q8_scale + up256(decode ? (size_t)B * Hq * sizeof(float) : 0);
+  s.part = s.counters + up256(chunk ? 2 * kChunkCtas * sizeof(ChunkMeta) : rows * sizeof(int));
+  s.q8 = s.part + up256((chunk ? (size_t)4 * kChunkCtas * kChunkPart : (rows + kMaxCtas) * G * kPartFloats) * sizeof(float));
+  s.q8_scale = s.q8 + up256(chunk ? 0 : (size_t)B * Hq * 2 * kD);
+  s.bytes = s.q8_scale + up256(chunk ? 0 : (size_t)B * Hq * sizeof(float));
   return s;
 }
+
+// The forms a call runs (bit 0: decode, bit 1: chunk). With more than one new token allowed, the
+// chunk form can take every sequence. A large batch likely decodes most of them, which the
+// decode form streams faster: 30 decode tokens at 100 to 4000 cached beside two chunks of 300 to
+// 512 take 98 us with both forms and 136 us with the chunk form alone (e4m3: 87 and 165). When
+// there are none, both cost two launches more: 8 x 7 tokens at 100 to 4000 cached 44 and 42 us,
+// four tiny prompts 27 and 16 us.
+constexpr int kMixedBatch = 16;
+int forms_of(int B, int max_q) { return max_q == 1 ? 1 : B >= kMixedBatch ? 3 : 2; }
 
 // Tensor maps of the pages: full-tile boxes of min(page, 128) rows and 16-row boxes.
 int page_maps(const KvPages& kv, CUtensorMap* k, CUtensorMap* v, CUtensorMap* k16, CUtensorMap* v16) {
@@ -1732,15 +1730,13 @@ int launch_decode(const PagedAttn& a, const CUtensorMap& tmQ, cudaStream_t s) {
 }
 
 int attention_decode(const PagedAttn& a, cudaStream_t s) {
-  const int G = a.Hq / a.kv.Hkv, B = a.pb.B;
+  const int G = 1 << a.g_shift, B = a.pb.B;
   CUtensorMap tmQ;
   if (a.kv.fp8 ? make_tmap_bytes(&tmQ, a.q8, (long long)B * a.Hq * 2, kD, 2 * G)
                : make_tmap_3d(&tmQ, a.q, kD, a.Hq, a.n_tokens, kD * 2, a.ldq * 2, 64, G, 1)) {
     set_last_error("attention_paged: cannot encode the query tensor map");
     return -6;
   }
-  const long long split = a.kv.fp8 ? ((long long)B * a.Hq + kPlanThreads / 32 - 1) / (kPlanThreads / 32) : 0;
-  q3_launch(paged_decode_prep_kernel, (unsigned)(1 + split), kPlanThreads, 0, s, a);
   switch (G * 2 + a.kv.fp8) {
     case 2: return launch_decode<1, false>(a, tmQ, s);
     case 3: return launch_decode<1, true>(a, tmQ, s);
@@ -1773,7 +1769,6 @@ int attention_chunk(const PagedAttn& a, cudaStream_t s) {
       return -6;
     }
   }
-  q3_launch(paged_chunk_plan_kernel, 1, kPlanThreads, 0, s, a);
   q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmK, tmV, tmK16, tmV16, a);
   q3_launch(paged_chunk_join_kernel, a.n_cta * 16, 128, 0, s, a);
   return 0;
@@ -1781,32 +1776,47 @@ int attention_chunk(const PagedAttn& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_attention_bytes(int B, int Hq, int Hkv, int max_q) { return scratch_of(B, Hq, Hkv, max_q).bytes; }
+size_t paged_attention_bytes(int B, int Hq, int Hkv, int max_q) {
+  const int forms = forms_of(B, max_q);
+  return (forms & 1 ? scratch_of(false, B, Hq, Hkv).bytes : 0) + (forms & 2 ? scratch_of(true, B, Hq, Hkv).bytes : 0);
+}
 
 int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int max_q, const PagedBatch& pb,
                            const KvPages& kv, int Hq, void* scratch, uint16_t* out, long long ldo, int* err,
                            cudaStream_t s, bool o_f16) {
-  const Scratch off = scratch_of(pb.B, Hq, kv.Hkv, max_q);
-  uint8_t* base = static_cast<uint8_t*>(scratch);
-  PagedAttn a;
-  a.pb = pb;
-  a.kv = kv;
-  a.n_tokens = n_tokens; a.max_q = max_q; a.Hq = Hq; a.o_f16 = o_f16 ? 1 : 0;
-  a.g_shift = 0;
-  while ((kv.Hkv << a.g_shift) < Hq) ++a.g_shift;
-  a.q = q; a.ldq = ldq;
-  a.out = out; a.ldo = ldo;
-  a.plan = reinterpret_cast<long long*>(base + off.plan);
-  a.start = reinterpret_cast<CtaStart*>(base + off.start);
-  const int cap = max_q == 1 ? kMaxCtas : kChunkCtas;
-  a.n_cta = num_sms() < cap ? num_sms() : cap;
-  a.meta = reinterpret_cast<ChunkMeta*>(base + off.counters);
-  a.counters = reinterpret_cast<int*>(base + off.counters);
-  a.part = reinterpret_cast<float*>(base + off.part);
-  a.q8 = base + off.q8;
-  a.q8_scale = reinterpret_cast<float*>(base + off.q8_scale);
-  a.err = err;
-  const int rc = max_q == 1 ? attention_decode(a, s) : kv.fp8 ? attention_chunk<true>(a, s) : attention_chunk<false>(a, s);
+  PagedAttn base = {};
+  base.pb = pb;
+  base.kv = kv;
+  base.n_tokens = n_tokens; base.max_q = max_q; base.Hq = Hq; base.o_f16 = o_f16 ? 1 : 0;
+  while ((kv.Hkv << base.g_shift) < Hq) ++base.g_shift;
+  base.q = q; base.ldq = ldq;
+  base.out = out; base.ldo = ldo;
+  base.err = err;
+  const int forms = forms_of(pb.B, max_q);
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  PagedAttn form[2] = {base, base};  // decode, chunk
+  for (int f = 0; f < 2; ++f) {
+    if (!(forms >> f & 1)) continue;
+    const Scratch off = scratch_of(f == 1, pb.B, Hq, kv.Hkv);
+    PagedAttn& a = form[f];
+    a.plan = reinterpret_cast<long long*>(ws + off.plan);
+    a.start = reinterpret_cast<CtaStart*>(ws + off.start);
+    a.counters = reinterpret_cast<int*>(ws + off.counters);
+    a.meta = reinterpret_cast<ChunkMeta*>(ws + off.counters);
+    a.part = reinterpret_cast<float*>(ws + off.part);
+    a.q8 = ws + off.q8;
+    a.q8_scale = reinterpret_cast<float*>(ws + off.q8_scale);
+    const int cap = f == 1 ? kChunkCtas : kMaxCtas;
+    a.n_cta = num_sms() < cap ? num_sms() : cap;
+    ws += off.bytes;
+  }
+  form[1].beside = forms == 3 ? 1 : 0;
+  form[1].min_q = forms == 3 ? 2 : 1;
+  const long long split = forms & 1 && kv.fp8 ? ((long long)pb.B * Hq + kPlanThreads / 32 - 1) / (kPlanThreads / 32) : 0;
+  q3_launch(paged_plan_kernel, (unsigned)(2 + split), kPlanThreads, 0, s, form[0], form[1], forms);
+  int rc = 0;
+  if (forms & 1) rc = attention_decode(form[0], s);
+  if (!rc && forms & 2) rc = kv.fp8 ? attention_chunk<true>(form[1], s) : attention_chunk<false>(form[1], s);
   if (rc) return rc;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

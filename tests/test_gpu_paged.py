@@ -159,7 +159,9 @@ def test_attention_group_sizes(q3, hq, hkv, fp8, qmax):
 # chunks: one row to several tiles, contexts of none to many pages, mixed with decode rows
 CHUNKS = [([2], [0], 16), ([64], [0], 16), ([65], [63], 32), ([128], [128], 128), ([129], [1], 256),
           ([300], [0], 64), ([1, 200, 0, 3, 77], [900, 33, 40, 0, 129], 16), ([7, 7, 7], [2000, 3, 500], 128),
-          ([1000], [1500], 64), ([17], [9000], 32)]
+          ([1000], [1500], 64), ([17], [9000], 32),
+          ([1, 90, 1, 1, 0, 1, 2, 1, 1, 64, 1, 1, 1, 1, 1, 1, 3, 1], [700, 300, 0, 5, 9, 2000, 127, 128, 64, 0, 31, 1, 900, 77, 255, 256, 10, 63], 16),
+          ([1] * 16 + [2], [40 * i for i in range(17)], 128), ([5] * 20, [33 * i for i in range(20)], 64)]
 
 
 @pytest.mark.parametrize("fp8", [False, True])
