@@ -14,8 +14,10 @@ namespace q3 {
 
 namespace {
 
-// Rows of 128 values in flight per warp: 4 (token, head) rows at a time, 8 lanes each.
-constexpr int kSlotsPerWarp = 8;
+// Rows of 128 values in flight per warp: 4 (token, head) rows at a time, 8 lanes each, of a
+// token's slots. At 6.5 TB/s and about 2 us from a warp's first load to its last store an SM
+// needs some 90 KB in flight: 4 KB a warp (2 KB reached 4.2 TB/s on 8192 tokens).
+constexpr int kSlotsPerWarp = 16;
 constexpr int kWarps = 8;
 
 struct NormRopeArgs {
@@ -33,19 +35,25 @@ struct NormRopeArgs {
   int* err;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
-  f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+// 8 bf16 as four pairs of fp32, and back
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack(w[i] << 16, w[i] & 0xffff0000u);
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+  return make_uint4(pack_bf16x2(f2_lo(f[0]), f2_hi(f[0])), pack_bf16x2(f2_lo(f[1]), f2_hi(f[1])),
+                    pack_bf16x2(f2_lo(f[2]), f2_hi(f[2])), pack_bf16x2(f2_lo(f[3]), f2_hi(f[3])));
 }
 // x * inv as e4m3, 8 values
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
+__device__ __forceinline__ uint2 quant8(const uint64_t (&f)[4], float inv) {
+  const uint64_t inv2 = f2_pack(__float_as_uint(inv), __float_as_uint(inv));
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = f2_mul(f[i], inv2);
+    w[i] = pack_e4m3x2(f2_lo(v), f2_hi(v));
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -77,51 +85,60 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_paged_kernel(const N
       hi[i] = *reinterpret_cast<const uint4*>(row + 64 + d);
     }
   }
-  const int b = paged_seq_of(a.pb, tok, lane);
-  if (b >= a.pb.B) return;  // a row behind the last sequence
-  const int t = tok - a.pb.q_start[b];
-  const int pos = a.pb.ctx_len[b] + t;
+  PagedToken at;
+  if (!paged_seq_of(a.pb, tok, lane, &at)) return;  // a row behind the last sequence
+  const int t = tok - at.start;
+  const int pos = at.ctx + t;
   if (t < 0 || pos >= a.max_pos) {
     if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
     return;
   }
-  const long long cell = paged_row(a.pb, a.kv, b, pos, lane == 0 ? a.err : nullptr);
-  if (cell < 0) return;
-  float cs[8], sn[8];
+  uint64_t cs[4], sn[4];  // of dims d + 2 j, d + 2 j + 1
   {
-    const float4* r = reinterpret_cast<const float4*>(a.rope + ((long long)pos * 64 + d) * 2);
+    // (a negative position is reported below; its row is not read)
+    const float4* r = reinterpret_cast<const float4*>(a.rope + ((long long)max(pos, 0) * 64 + d) * 2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = r[i];
-      cs[2 * i] = v.x; sn[2 * i] = v.y; cs[2 * i + 1] = v.z; sn[2 * i + 1] = v.w;
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = r[j];
+      cs[j] = f2_pack(__float_as_uint(v.x), __float_as_uint(v.z));
+      sn[j] = f2_pack(__float_as_uint(v.y), __float_as_uint(v.w));
     }
   }
+  const long long cell = paged_row(a.pb, a.kv, at.b, pos, lane == 0 ? a.err : nullptr);
+  if (cell < 0) return;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int slot = slot0 + 4 * i;
-    float x[8], y[8];
+    const bool is_q = slot < a.Hq, is_v = slot >= a.Hq + Hkv;
+    // two values an instruction: these operations, not the bytes, bound the plain form
+    uint64_t x[4], y[4];
     unpack8(lo[i], x);
     unpack8(hi[i], y);
-    const bool is_q = slot < a.Hq, is_v = slot >= a.Hq + Hkv;
-    float ss = 0.f;
+    if (__any_sync(0xffffffffu, !is_v)) {
+      uint64_t s2 = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += x[j] * x[j] + y[j] * y[j];
+      for (int j = 0; j < 4; ++j) s2 = f2_fma(y[j], y[j], f2_fma(x[j], x[j], s2));
+      float ss = f2_lo(s2) + f2_hi(s2);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (slot >= slots) continue;
-    if (!is_v) {
-      const float r = rsqrtf(ss * (1.0f / 128.0f) + a.eps);
-      const uint16_t* wn = is_q ? a.qw : a.kw;
-      float wx[8], wy[8];
-      unpack8(*reinterpret_cast<const uint4*>(wn + d), wx);
-      unpack8(*reinterpret_cast<const uint4*>(wn + 64 + d), wy);
+      for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!is_v) {
+        const float r = rsqrtf(ss * (1.0f / 128.0f) + a.eps);
+        const uint64_t r2 = f2_pack(__float_as_uint(r), __float_as_uint(r));
+        const uint64_t n2 = f2_pack(__float_as_uint(-r), __float_as_uint(-r));
+        const uint16_t* wn = is_q ? a.qw : a.kw;
+        uint64_t wx[4], wy[4];
+        unpack8(*reinterpret_cast<const uint4*>(wn + d), wx);
+        unpack8(*reinterpret_cast<const uint4*>(wn + 64 + d), wy);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = x[j] * r * wx[j], w = y[j] * r * wy[j];
-        x[j] = u * cs[j] - w * sn[j];
-        y[j] = u * sn[j] + w * cs[j];
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t u = f2_mul(x[j], wx[j]), w = f2_mul(y[j], wy[j]);
+          const uint64_t c = f2_mul(cs[j], r2), s = f2_mul(sn[j], r2), ns = f2_mul(sn[j], n2);
+          x[j] = f2_fma(w, ns, f2_mul(u, c));
+          y[j] = f2_fma(w, c, f2_mul(u, s));
+        }
       }
     }
+    if (slot >= slots) continue;
     if (is_q) {
       uint16_t* dst = a.q_out + tok * a.ldq + (long long)slot * 128;
       *reinterpret_cast<uint4*>(dst + d) = pack8(x);
@@ -168,10 +185,11 @@ int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens
 // ---------------------------------------------------------------------------
 // Copies between pages and a contiguous cache [B][Hkv][s_max][128] bf16: the batch's new
 // positions of every head, k and v. 16 lanes per row of 128 values (16 bytes of bf16, 8 of
-// e4m3, a lane), 8 rows in flight per warp: the 2 Hkv rows of a token go to ceil(2 Hkv / 8)
-// warps.
+// e4m3, a lane), kRows rows in flight per warp: the 2 Hkv rows of a token go to
+// ceil(2 Hkv / kRows) warps.
 // ---------------------------------------------------------------------------
 namespace {
+constexpr int kRows = 16;
 struct MoveArgs {
   PagedBatch pb;
   KvPages kv;
@@ -191,21 +209,21 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
   const int tok = (int)(item / a.n_blocks_tok);
   if (tok >= a.n_tokens) return;
   const int Hkv = a.kv.Hkv;
-  const int b = paged_seq_of(a.pb, tok, lane);
-  if (b >= a.pb.B) return;
-  const int t = tok - a.pb.q_start[b];
-  const int pos = a.pb.ctx_len[b] + t;
+  PagedToken at;
+  if (!paged_seq_of(a.pb, tok, lane, &at)) return;
+  const int b = at.b, t = tok - at.start;
+  const int pos = at.ctx + t;
   if (t < 0 || pos >= a.s_max) {
     if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
     return;
   }
   const long long cell = paged_row(a.pb, a.kv, b, pos, lane == 0 ? a.err : nullptr);
   if (cell < 0) return;
-  const int row0 = (int)(item % a.n_blocks_tok) * 8 + (lane >> 4);
+  const int row0 = (int)(item % a.n_blocks_tok) * kRows + (lane >> 4);
   const int d = (lane & 15) * 8;
-  uint4 in[4];
+  uint4 in[kRows / 2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kRows / 2; ++i) {
     const int r = row0 + 2 * i;
     if (r >= 2 * Hkv) continue;
     const bool is_v = r >= Hkv;
@@ -222,7 +240,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kRows / 2; ++i) {
     const int r = row0 + 2 * i;
     if (r >= 2 * Hkv) continue;
     const bool is_v = r >= Hkv;
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
     uint16_t* cont = is_v ? a.cv : a.ck;
     if (FP8) {
       const float scale = (is_v ? a.kv.v_scale : a.kv.k_scale)[h];
-      float f[8];
+      uint64_t f[4];
       if (TO_PAGES) {
         unpack8(in[i], f);
         *reinterpret_cast<uint2*>(pool + paged * 128 + d) = quant8(f, 1.0f / scale);
@@ -242,8 +260,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 p = e4m3x2_to_f32x2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-          f[2 * j] = p.x * scale;
-          f[2 * j + 1] = p.y * scale;
+          f[j] = f2_pack(__float_as_uint(p.x * scale), __float_as_uint(p.y * scale));
         }
         *reinterpret_cast<uint4*>(cont + flat * 128 + d) = pack8(f);
       }
@@ -264,7 +281,7 @@ int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_t
   a.cv = cv;
   a.s_max = s_max;
   a.n_tokens = n_tokens;
-  a.n_blocks_tok = (2 * kv.Hkv + 7) / 8;
+  a.n_blocks_tok = (2 * kv.Hkv + kRows - 1) / kRows;
   a.err = err;
   const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
   if (blocks >= (1ll << 31)) {

@@ -25,17 +25,27 @@ struct KvPages {
   int n_pages, page_shift, Hkv, fp8;
 };
 
-// Number of sequences that end at or before row `tok` (q_start is non-decreasing): the
-// sequence holding the row, or B behind the last one. Every lane of the warp calls it.
-__device__ __forceinline__ int paged_seq_of(const PagedBatch& pb, int tok, int lane) {
-  int n = 0;
+// The sequence holding row `tok` (the first that ends behind it; q_start is non-decreasing), with
+// its first row and cached length. Every lane of the warp calls it: 32 sequences a round,
+// one memory latency each. False for a row behind the last sequence.
+struct PagedToken {
+  int b, start, ctx;
+};
+__device__ __forceinline__ bool paged_seq_of(const PagedBatch& pb, int tok, int lane, PagedToken* out) {
   for (int base = 0; base < pb.B; base += 32) {
     const int i = base + lane;
-    const unsigned ended = __ballot_sync(0xffffffffu, i < pb.B && pb.q_start[i + 1] <= tok);
-    n += __popc(ended);
-    if (ended != 0xffffffffu) break;
+    const bool in = i < pb.B;
+    const int end = in ? pb.q_start[i + 1] : 0, first = in ? pb.q_start[i] : 0, ctx = in ? pb.ctx_len[i] : 0;
+    const unsigned here = __ballot_sync(0xffffffffu, in && end > tok);
+    if (here) {
+      const int f = __ffs(here) - 1;
+      out->b = base + f;
+      out->start = __shfl_sync(0xffffffffu, first, f);
+      out->ctx = __shfl_sync(0xffffffffu, ctx, f);
+      return true;
+    }
   }
-  return n;
+  return false;
 }
 
 // Index of the cache row [page][0][slot] of position pos of sequence b (add head *
