@@ -267,22 +267,24 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
 // cost in precision is bought back in the columns, which are nearly free here: q enters as
 // two e4m3 terms (exact for bf16 queries) and P as three, each 16 times finer than the last
 // (P scaled so that the running maximum is 2^5 to 2^8 of e4m3's 448: relative error 2^-12, or
-// 2^-23 of the row's largest weight, finer than bf16), in columns [t G, t G + G) of term t.
+// 2^-23 of the row's largest weight, finer than bf16), in columns [t G, t G + G) of term t. With
+// bf16 pages P enters as two bf16 terms, hi and the rest (2^-16), in the same way.
 // Two TMA warps fill rings of K and of V tiles, one box per page; one warp issues S, one P.V; two sets of softmax warps take alternate tiles,
 // a thread owning one key (S) and one head dim (O). A row that spans CTAs leaves partials; the last of them to arrive merges
 // them in CTA order, so the result does not depend on which one that is, and nobody waits.
 // ============================================================================
 template <int G, bool FP8>
 struct DecodeCfg {
-  static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 1;
-  static constexpr int kCols = (kPTerms * G + 15) / 16 * 16;          // MMA N
+  static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 2;
+  static constexpr int kSCols = (kQTerms * G + 15) / 16 * 16;         // N of S
+  static constexpr int kCols = (kPTerms * G + 15) / 16 * 16;          // N of P.V
   static constexpr int kHeadWarps = G >= 8 ? 2 : 1;                   // softmax warps of a set per lane quarter
   static constexpr int kSetWarps = 4 * kHeadWarps;
   static constexpr int kSoftmaxWarps = 2 * kSetWarps;                 // set X takes the CTA's tiles of parity X
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kStages = FP8 ? (G == 16 ? 5 : 6) : 3;
   static constexpr uint32_t kKV = FP8 ? kTile8 : 2 * kTile8;          // K or V of one tile
-  static constexpr uint32_t kQB = (FP8 ? 1 : 2) * kCols * 128;        // q of one row
+  static constexpr uint32_t kQB = (FP8 ? 1 : 2) * kSCols * 128;       // q of one row
   static constexpr uint32_t kOffV = kStages * kKV;                    // K ring, V ring, q of two rows
   static constexpr uint32_t kOffQ = 2 * kStages * kKV;
   static constexpr uint32_t kPB = (FP8 ? 1 : 2) * kCols * 128;        // one P buffer
@@ -292,7 +294,7 @@ struct DecodeCfg {
   static constexpr uint32_t kOffBar = kOffX + G * kD * 4 + 2 * 16 * 4;
   static constexpr uint32_t kSmem = kOffBar + (4 * kStages + 14) * 8 + 16 + 1024;
   // tensor memory: S of set 0 and 1, O of set 0 and 1
-  static constexpr uint32_t kTmem = 4 * kCols <= 64 ? 64 : (4 * kCols <= 128 ? 128 : 256);
+  static constexpr uint32_t kTmem = 2 * (kSCols + kCols) <= 64 ? 64 : (2 * (kSCols + kCols) <= 128 ? 128 : 256);
 };
 
 // Walk over the (sequence, group) rows that meet this CTA's tiles: tiles [j0, j1) of the row.
@@ -392,7 +394,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
                              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
                              const __grid_constant__ CUtensorMap tmV16, const PagedAttn a) {
   using C = DecodeCfg<G, FP8>;
-  constexpr int SW = C::kSoftmaxWarps, XW = C::kSetWarps, HW = C::kHeadWarps, GH = G / HW, NC = C::kCols, NS = C::kStages;
+  constexpr int SW = C::kSoftmaxWarps, XW = C::kSetWarps, HW = C::kHeadWarps, GH = G / HW, NC = C::kCols, SC = C::kSCols,
+                NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] K (and q) loaded
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tmO = tmem + 2 * NC;
+  const uint32_t tmO = tmem + 2 * SC;
   pdl_wait();
   pdl_trigger();
   const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
             tma_load_2d(dst, &tmQ, &q_full[qs], 0, (b * Hkv + g) * 2 * G);
           } else {
             tma_load_3d(dst, &tmQ, &q_full[qs], 0, g * G, tok);
-            tma_load_3d(dst + NC * 128, &tmQ, &q_full[qs], 64, g * G, tok);
+            tma_load_3d(dst + SC * 128, &tmQ, &q_full[qs], 64, g * G, tok);
           }
         }
         __syncwarp();
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
   } else if (warp == SW + 1) {
     if (elect_one()) {
       // ------------------------------------------------------------ S issuer: S = K q
-      constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, NC, 0, 0) : idesc_bf16_f32(128, NC, 0, 0);
+      constexpr uint32_t idesc = FP8 ? idesc_e4m3_f32(128, SC, 0, 0) : idesc_bf16_f32(128, SC, 0, 0);
       int tc = 0, st = 0, rows_seen = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -554,13 +557,13 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           if (FP8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_e4m3_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK) + 2 * kk, sdesc_kmajor_sw128(sQ) + 2 * kk, idesc,
+              mma_e4m3_ss(tmem + SC * sb, sdesc_kmajor_sw128(sK) + 2 * kk, sdesc_kmajor_sw128(sQ) + 2 * kk, idesc,
                           kk ? 1u : 0u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(tmem + NC * sb, sdesc_kmajor_sw128(sK + (kk >> 2) * kTile8) + 2 * (kk & 3),
-                          sdesc_kmajor_sw128(sQ + (kk >> 2) * NC * 128) + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+              mma_bf16_ss(tmem + SC * sb, sdesc_kmajor_sw128(sK + (kk >> 2) * kTile8) + 2 * (kk & 3),
+                          sdesc_kmajor_sw128(sQ + (kk >> 2) * SC * 128) + 2 * (kk & 3), idesc, kk ? 1u : 0u);
           }
           mma_commit(&s_full[sb]);
           mma_commit(&k_empty[st]);
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     const int X = warp / XW, qd = warp & 3, hh = (warp % XW) >> 2, j0 = hh * GH;
     const int t = qd * 32 + lane;
     const uint32_t lanes = (uint32_t)(qd * 32) << 16;
-    const uint32_t tS = tmem + lanes + NC * X, tO = tmO + lanes + NC * X;
+    const uint32_t tS = tmem + lanes + SC * X, tO = tmO + lanes + NC * X;
     float* red_max = reinterpret_cast<float*>(smem + C::kOffRed) + X * 3 * 64;  // [2][4][16]
     float* red_sum = red_max + 2 * 64;                                          // [4][16]
     float* x_o = reinterpret_cast<float*>(smem + C::kOffX);                     // [G][128]
@@ -629,7 +632,6 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     uint8_t* p_buf = smem + C::kOffP + X * C::kPB;
     // e4m3: the running maximum is kept 5 below the scores', so that P lies in (0, 2^8]
     constexpr float kShift = FP8 ? 5.f : 0.f;
-    constexpr int kSCols = (C::kQTerms * G + 15) / 16 * 16;
     int tc0 = 0;  // the CTA's tiles before the current row
     int u = 0;    // the set's tiles so far
     bool ok = true;
@@ -649,12 +651,12 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         const uint32_t par = (uint32_t)(u & 1);
         ok = ok && !*s_abort && mbar_wait(&s_full[X], par, err);
         ok = __all_sync(0xffffffffu, ok);
-        uint32_t sv[kSCols];
+        uint32_t sv[SC];
 #pragma unroll
-        for (int i = 0; i < kSCols; ++i) sv[i] = 0u;
+        for (int i = 0; i < SC; ++i) sv[i] = 0u;
         if (ok) {
           tc_fence_after();
-          tmem_ld_cols<kSCols>(tS, sv);
+          tmem_ld_cols<SC>(tS, sv);
         }
         tc_fence_before();
         arrive_warp(&s_empty[X], lane);
@@ -728,8 +730,11 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
             const int chunk = (t & 63) >> 3;
 #pragma unroll
             for (int jj = 0; jj < GH; ++jj) {
-              const int row = j0 + jj;
-              *reinterpret_cast<uint16_t*>(pb + row * 128 + ((chunk ^ (row & 7)) << 4)) = to_bf16_bits(p[jj]);
+              const int row = j0 + jj, low = G + row;
+              const uint16_t hi = to_bf16_bits(p[jj]);
+              *reinterpret_cast<uint16_t*>(pb + row * 128 + ((chunk ^ (row & 7)) << 4)) = hi;
+              *reinterpret_cast<uint16_t*>(pb + low * 128 + ((chunk ^ (low & 7)) << 4)) =
+                  to_bf16_bits(p[jj] - __uint_as_float((uint32_t)hi << 16));
             }
           }
           // keys past the last one: zero their V rows (0 * NaN would poison O)
@@ -773,11 +778,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 #pragma unroll
       for (int jj = 0; jj < GH; ++jj) {
         const int hd = j0 + jj;
-        o[jj] = pick<HW, GH>(ov, 0, hh, jj);
-        if (FP8) {
-          o[jj] += pick<HW, GH>(ov, FP8 ? G : 0, hh, jj) * 0.0625f;
-          o[jj] += pick<HW, GH>(ov, FP8 ? 2 * G : 0, hh, jj) * 0.00390625f;
-        }
+        o[jj] = pick<HW, GH>(ov, 0, hh, jj) + pick<HW, GH>(ov, G, hh, jj) * (FP8 ? 0.0625f : 1.f);
+        if (FP8) o[jj] += pick<HW, GH>(ov, FP8 ? 2 * G : 0, hh, jj) * 0.00390625f;
         l[jj] = red_sum[hd] + red_sum[16 + hd] + red_sum[32 + hd] + red_sum[48 + hd];
       }
       // set 1 hands its half of the row to set 0, which carries on with the whole

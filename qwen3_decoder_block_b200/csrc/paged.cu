@@ -16,9 +16,11 @@ namespace {
 
 // Rows of 128 values in flight per warp: 4 (token, head) rows at a time, 8 lanes each, of a
 // token's slots. At 6.5 TB/s and about 2 us from a warp's first load to its last store an SM
-// needs some 90 KB in flight: 4 KB a warp (2 KB reached 4.2 TB/s on 8192 tokens).
+// needs some 90 KB in flight: 4 KB a warp, 24 warps an SM (80 registers), in small blocks that
+// are replaced one by one. 8192 tokens: 28.3 us (4.8 TB/s); 2 KB a warp or blocks of 256 31 to 32 us.
 constexpr int kSlotsPerWarp = 16;
-constexpr int kWarps = 8;
+constexpr int kNormWarps = 4;
+constexpr int kWarps = 8;  // of the moves
 
 struct NormRopeArgs {
   PagedBatch pb;
@@ -64,11 +66,11 @@ __device__ __forceinline__ uint2 quant8(const uint64_t (&f)[4], float inv) {
 // each load of 16 bytes is part of 128 contiguous ones, and the sum of squares takes three
 // shuffles. A warp owns kSlotsPerWarp consecutive head slots of a token.
 template <bool FP8>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_paged_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(32 * kNormWarps, 6) qk_norm_rope_paged_kernel(const NormRopeArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long item = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
   const int tok = (int)(item / a.n_blocks_tok);
   if (tok >= a.n_tokens) return;
   const int Hkv = a.kv.Hkv, slots = a.Hq + 2 * Hkv;
@@ -172,13 +174,13 @@ int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens
   a.n_blocks_tok = (Hq + 2 * kv.Hkv + kSlotsPerWarp - 1) / kSlotsPerWarp;
   a.eps = eps;
   a.err = err;
-  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
+  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kNormWarps - 1) / kNormWarps;
   if (blocks >= (1ll << 31)) {
     set_last_error("qk_norm_rope_paged: %d tokens exceed the grid limit", n_tokens);
     return -2;
   }
   q3_launch(kv.fp8 ? qk_norm_rope_paged_kernel<true> : qk_norm_rope_paged_kernel<false>, (unsigned)blocks,
-            32 * kWarps, 0, s, a);
+            32 * kNormWarps, 0, s, a);
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 
