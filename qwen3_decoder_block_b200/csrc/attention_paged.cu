@@ -330,7 +330,12 @@ struct RowWalk {
 // up at one shared-memory word).
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
+  // predicated, not branched: the lanes stay together
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(lane)
+      : "memory");
 }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
@@ -1340,6 +1345,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
       const bool valid = r < n_rows;
       const bool warp_valid = quad * 32 < n_rows;
       const int qpos = valid ? w.ctx + tile_t0 + (r >> gs) : w.n_keys - 1;
+      const int qpos_first = __shfl_sync(0xffffffffu, qpos, 0);  // the warp's smallest
       q_loads0 += w.loads_q(0);
       float factor = kScaleLog2;
       if (w.loads_q(X)) {
@@ -1415,98 +1421,97 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
       }
       float m_run = -INFINITY, l_run = 0.f;
       const int kb = w.first(X), ke = w.end(X), step = w.step();
-      for (int k = kb; k < ke; k += step) {
-        const int nh = w.halves(X, k);
-        for (int h = 0; h < nh; ++h, ++u) {
-          const int bi = 2 * X + (u & 1);
-          const uint32_t tSb = tS + 64 * (u & 1);
-          const int kv0 = k * kTileK + 64 * h;
-          ok = ok && !*s_abort && mbar_wait(&s_full[bi], (uint32_t)((u >> 1) & 1), err);
-          ok = __all_sync(0xffffffffu, ok);
-          // bf16 V: zero the tile's rows past the last key (0 * NaN would poison O); both
-          // warpgroups of a pair do so before they release their P (zeros over zeros)
-          if (!FP8 && h == 0 && kv0 + kTileK > w.n_keys) {
-            const int c = c0 + (k - w.k0), st = c % NV;
-            ok = __all_sync(0xffffffffu, ok && !*s_abort && mbar_wait(&v_full[st], (uint32_t)((c / NV) & 1), err));
-            if (ok && kv0 + r >= w.n_keys) {
-              uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
+      // the half tiles in order: keys kv0 .. kv0 + 63 (the loop carries little: its serial
+      // instructions, not the waits, are what a half tile costs besides its exponentials)
+      const int n_half = kb < ke ? 2 * ((ke - kb - 1) / step) + w.halves(X, kb + (ke - kb - 1) / step * step) : 0;
+      int kv0 = kb * kTileK;
+      for (int n = 0; n < n_half; ++n, ++u, kv0 += n & 1 ? 64 : step * kTileK - 64) {
+        const int bi = 2 * X + (u & 1);
+        const uint32_t tSb = tS + 64 * (u & 1);
+        ok = ok && mbar_wait_warp(&s_full[bi], (uint32_t)((u >> 1) & 1), err);
+        // bf16 V: zero the tile's rows past the last key (0 * NaN would poison O); both
+        // warpgroups of a pair do so before they release their P (zeros over zeros)
+        if (!FP8 && kv0 + kTileK > w.n_keys && !(n & 1)) {
+          const int c = c0 + ((kv0 >> 7) - w.k0), st = c % NV;
+          ok = ok && mbar_wait_warp(&v_full[st], (uint32_t)((c / NV) & 1), err);
+          if (ok && kv0 + r >= w.n_keys) {
+            uint4* v0 = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kVTile + r * 128);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
+            for (int i = 0; i < 8; ++i) v0[i] = v0[i + kTile8 / 16] = make_uint4(0, 0, 0, 0);
           }
-          if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
-            tc_fence_before();
-            arrive_warp(&p_full[bi], lane);
-            continue;
-          }
-          tc_fence_after();
-          const bool need_mask = __any_sync(0xffffffffu, kv0 + 63 > qpos);
-          uint32_t v[2][32];
-          tmem_ld32(tSb, v[0]);
-          tmem_ld32(tSb + 32, v[1]);
-          tmem_wait_ld_regs(v[0]);
-          tmem_wait_ld_regs(v[1]);
-          if (need_mask) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (kv0 + c * 32 + i > qpos) v[c][i] = __float_as_uint(-INFINITY);
-          }
-          float mc[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
-            mc[c] = __uint_as_float(x[0]);
-#pragma unroll
-            for (int i = 1; i < 15; i += 2) mc[c] = fmax3(mc[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            mc[c] = fmaxf(mc[c], __uint_as_float(x[15]));
-          }
-          const float mxs = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * factor - kShift;
-          float alpha = 1.f;
-          if (mxs > m_run + kRescaleThreshold || m_run == -INFINITY) {
-            alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mxs);
-            m_run = mxs;
-          }
-          // p = 2^(s factor - m); a row that has seen no key yet (its causal limit lies before
-          // this half tile) keeps m = -inf and p = 2^-inf = 0
-          const float neg = m_run == -INFINITY ? 0.f : -m_run;
-          const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
-          const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
-          uint64_t acc2[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const uint64_t e = f2_fma(f2_pack(v[c][i], v[c][i + 1]), scale2, neg2);
-              const float p0 = ex2_approx(f2_lo(e));
-              const float p1 = ex2_approx(f2_hi(e));
-              acc2[(i >> 1) & 1] = f2_add(acc2[(i >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-              v[c][i >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-            }
-            tmem_st16(tSb + c * 16, v[c]);
-          }
-          const uint64_t acc = f2_add(acc2[0], acc2[1]);
-          l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
-          if ((k > kb || h) && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // O_X is stable once the previous half tile's P.V is complete
-            ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(&pv_done[bi ^ 1], (uint32_t)(((u - 1) >> 1) & 1), err));
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_wait_ld_regs(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + c * 32, o);
-            }
-          }
-          tmem_wait_st();
+          fence_proxy_async_smem();
+        }
+        if (!ok || !warp_valid) {  // (a warp of rows behind the last token only keeps step)
           tc_fence_before();
           arrive_warp(&p_full[bi], lane);
+          continue;
         }
+        tc_fence_after();
+        const bool need_mask = kv0 + 63 > qpos_first;
+        uint32_t v[2][32];
+        tmem_ld32(tSb, v[0]);
+        tmem_ld32(tSb + 32, v[1]);
+        tmem_wait_ld_regs(v[0]);
+        tmem_wait_ld_regs(v[1]);
+        if (need_mask) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (kv0 + c * 32 + i > qpos) v[c][i] = __float_as_uint(-INFINITY);
+        }
+        float mc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t* x = v[c >> 1] + 16 * (c & 1);
+          mc[c] = __uint_as_float(x[0]);
+#pragma unroll
+          for (int i = 1; i < 15; i += 2) mc[c] = fmax3(mc[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          mc[c] = fmaxf(mc[c], __uint_as_float(x[15]));
+        }
+        const float mxs = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * factor - kShift;
+        float alpha = 1.f;
+        if (mxs > m_run + kRescaleThreshold || m_run == -INFINITY) {
+          alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mxs);
+          m_run = mxs;
+        }
+        // p = 2^(s factor - m); a row that has seen no key yet (its causal limit lies before
+        // this half tile) keeps m = -inf and p = 2^-inf = 0
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+        const uint64_t scale2 = f2_pack(__float_as_uint(factor), __float_as_uint(factor));
+        const uint64_t neg2 = f2_pack(__float_as_uint(neg), __float_as_uint(neg));
+        uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t e = f2_fma(f2_pack(v[c][i], v[c][i + 1]), scale2, neg2);
+            const float p0 = ex2_approx(f2_lo(e));
+            const float p1 = ex2_approx(f2_hi(e));
+            acc2[(i >> 1) & 1] = f2_add(acc2[(i >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+            v[c][i >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tSb + c * 16, v[c]);
+        }
+        const uint64_t acc = f2_add(acc2[0], acc2[1]);
+        l_run = l_run * alpha + f2_lo(acc) + f2_hi(acc);
+        if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O_X is stable once the previous half tile's P.V is complete
+          ok = mbar_wait_warp(&pv_done[bi ^ 1], (uint32_t)(((u - 1) >> 1) & 1), err);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&p_full[bi], lane);
       }
       c0 += w.k1 - w.k0;
       const bool any = kb < ke;

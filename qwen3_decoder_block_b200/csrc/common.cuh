@@ -123,6 +123,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   return true;
 }
 
+// The same for a whole converged warp, for waits that mostly find the phase complete: one try, one
+// vote and no branch that the lanes could take apart.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+}
+
 // ----------------------------------------------------------------------------
 // TMA (tensor memory accelerator) loads, no multicast.
 // ----------------------------------------------------------------------------
