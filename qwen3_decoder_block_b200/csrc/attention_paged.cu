@@ -654,8 +654,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       for (int j = j_first; j < je; j += 2, ++u) {
         const int nk = min(kTileK, w.n_keys - j * kTileK);
         const uint32_t par = (uint32_t)(u & 1);
-        ok = ok && !*s_abort && mbar_wait(&s_full[X], par, err);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && mbar_wait_warp(&s_full[X], par, err);
         uint32_t sv[SC];
 #pragma unroll
         for (int i = 0; i < SC; ++i) sv[i] = 0u;
@@ -696,8 +695,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         }
         // the set's P buffer and O are free once the P.V of its previous tile is complete
         if (u >= 1) {
-          ok = ok && !*s_abort && mbar_wait(&pv_done[X], par ^ 1u, err);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = ok && mbar_wait_warp(&pv_done[X], par ^ 1u, err);
         }
         if (ok) {
           tc_fence_after();
@@ -745,7 +743,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
           // keys past the last one: zero their V rows (0 * NaN would poison O)
           if (hh == 0 && nk < kTileK) {
             const int tc = tc0 + (j - jb), st = tc % NS;
-            ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (uint32_t)((tc / NS) & 1), err));
+            ok = mbar_wait_warp(&v_full[st], (uint32_t)((tc / NS) & 1), err);
             if (ok && t >= nk) {
               uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kKV + t * 128);
 #pragma unroll
@@ -767,8 +765,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < NC; ++i) ov[i] = 0u;
       if (any) {
-        ok = ok && !*s_abort && mbar_wait(&pv_done[X], (uint32_t)((u - 1) & 1), err);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && mbar_wait_warp(&pv_done[X], (uint32_t)((u - 1) & 1), err);
         if (ok) {
           tc_fence_after();
           tmem_ld_cols<NC>(tO, ov);
