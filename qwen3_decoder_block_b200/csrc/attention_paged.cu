@@ -1634,32 +1634,64 @@ __global__ void __launch_bounds__(128) paged_chunk_join_kernel(const PagedAttn a
   pdl_trigger();
   const int cx = blockIdx.x >> 3, d0 = (blockIdx.x & 7) * 16, c = cx >> 1, X = cx & 1;
   const ChunkMeta m = a.meta[cx];
-  const int r = threadIdx.x;
-  if (!m.split || r >= m.n_rows) return;
+  const int r = threadIdx.x, lane = r & 31;
+  if (!m.split) return;
+  const bool valid = r < m.n_rows;
   auto part = [&](int i) { return a.part + ((long long)(i * 2 + (i == c ? 1 : 0)) * 2 + X) * kChunkPart; };
-  auto has = [&](int i) { return i == c || a.meta[i * 2 + X].has != 0; };
-  float M = -INFINITY;
-  for (int i = c; i <= m.c_last; ++i)
-    if (has(i)) M = fmaxf(M, __ldcg(part(i) + kD * 128 + r));
-  float L = 0.f, o[16];
+  float M = -INFINITY, L = 0.f, o[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) o[j] = 0.f;
-#pragma unroll 4
-  for (int i = c; i <= m.c_last; ++i) {
-    if (!has(i)) continue;
-    const float* p = part(i);
-    const float mi = __ldcg(p + kD * 128 + r), li = __ldcg(p + kD * 128 + 128 + r);
-    const float w = mi == -INFINITY ? 0.f : exp2f(mi - M);
-    L += li * w;
+  for (int base = c; base <= m.c_last; base += 32) {
+    const int i = base + lane;
+    unsigned left = __ballot_sync(0xffffffffu, i == c || (i <= m.c_last && a.meta[2 * i + X].has != 0));
+    // kBatch partials at a time, their loads in flight together (one after the other they cost
+    // three latencies each, 13 us for a call)
+    constexpr int kBatch = 4;
+    while (left) {
+      const float* p[kBatch];
+      float mi[kBatch], li[kBatch];
+      float4 v[kBatch][4];
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + (d0 + j) * 128 + r * 4));
-      o[j] += w != 0.f ? v.x * w : 0.f;
-      o[j + 1] += w != 0.f ? v.y * w : 0.f;
-      o[j + 2] += w != 0.f ? v.z * w : 0.f;
-      o[j + 3] += w != 0.f ? v.w * w : 0.f;
+      for (int b = 0; b < kBatch; ++b) {
+        const int f = __ffs(left) - 1;
+        left &= left - 1;
+        p[b] = f < 0 ? nullptr : part(base + f);
+        mi[b] = -INFINITY;
+        li[b] = 0.f;
+        if (valid && p[b]) {
+          mi[b] = __ldcg(p[b] + kD * 128 + r);
+          li[b] = __ldcg(p[b] + kD * 128 + 128 + r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[b][j] = __ldcg(reinterpret_cast<const float4*>(p[b] + (d0 + 4 * j) * 128 + r * 4));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[b][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) Mn = fmaxf(Mn, mi[b]);
+      const float old = M == -INFINITY ? 0.f : exp2f(M - Mn);
+      M = Mn;
+      L *= old;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] *= old;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float w = mi[b] == -INFINITY ? 0.f : exp2f(mi[b] - Mn);
+        L += li[b] * w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // (a row that saw no key of a part has weight 0 there, whatever its o holds)
+          o[4 * j] += w != 0.f ? v[b][j].x * w : 0.f;
+          o[4 * j + 1] += w != 0.f ? v[b][j].y * w : 0.f;
+          o[4 * j + 2] += w != 0.f ? v[b][j].z * w : 0.f;
+          o[4 * j + 3] += w != 0.f ? v[b][j].w * w : 0.f;
+        }
+      }
     }
   }
+  if (!valid) return;
   const int gs = a.g_shift, G = 1 << gs;
   const float mul = (a.kv.fp8 ? a.kv.v_scale[m.g] : 1.f) / L;
   uint16_t* dst = a.out + (long long)(m.tok + (r >> gs)) * a.ldo + (long long)(m.g * G + (r & (G - 1))) * kD + d0;
