@@ -186,12 +186,13 @@ int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens
 
 // ---------------------------------------------------------------------------
 // Copies between pages and a contiguous cache [B][Hkv][s_max][128] bf16: the batch's new
-// positions of every head, k and v. 16 lanes per row of 128 values (16 bytes of bf16, 8 of
-// e4m3, a lane), kRows rows in flight per warp: the 2 Hkv rows of a token go to
-// ceil(2 Hkv / kRows) warps.
+// positions of every head, k and v. A warp takes kHeads heads of a token: 16 lanes per row of
+// 128 values (16 bytes of bf16, 8 of e4m3, a lane), kHeads rows of k and as many of v in flight.
+// Instructions count here (issue slots were 63 to 77 % busy with addresses computed row by
+// row): two base addresses, stepped by constant strides.
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kRows = 16;
+constexpr int kHeads = 8;
 struct MoveArgs {
   PagedBatch pb;
   KvPages kv;
@@ -213,65 +214,66 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
   const int Hkv = a.kv.Hkv;
   PagedToken at;
   if (!paged_seq_of(a.pb, tok, lane, &at)) return;
-  const int b = at.b, t = tok - at.start;
+  const int t = tok - at.start;
   const int pos = at.ctx + t;
   if (t < 0 || pos >= a.s_max) {
     if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
     return;
   }
-  const long long cell = paged_row(a.pb, a.kv, b, pos, lane == 0 ? a.err : nullptr);
+  const long long cell = paged_row(a.pb, a.kv, at.b, pos, lane == 0 ? a.err : nullptr);
   if (cell < 0) return;
-  const int row0 = (int)(item % a.n_blocks_tok) * kRows + (lane >> 4);
+  constexpr int kIter = kHeads / 2;
+  const int h0 = (int)(item % a.n_blocks_tok) * kHeads + (lane >> 4);  // heads h0, h0 + 2, ...
   const int d = (lane & 15) * 8;
-  uint4 in[kRows / 2];
+  const int n = min(kIter, (Hkv - h0 + 1) >> 1);
+  constexpr int kCell = FP8 ? 1 : 2;  // bytes a value in the pages
+  const long long flat = (((long long)at.b * Hkv + h0) * a.s_max + pos) * 128 + d, flat_step = 256ll * a.s_max;
+  const long long page = ((cell + ((long long)h0 << a.kv.page_shift)) * 128 + d) * kCell,
+                  page_step = (256ll << a.kv.page_shift) * kCell;
+  uint16_t* flat_kv[2] = {a.ck + flat, a.cv + flat};
+  uint8_t* page_kv[2] = {a.kv.k + page, a.kv.v + page};
+  uint4 in[2][kIter];
 #pragma unroll
-  for (int i = 0; i < kRows / 2; ++i) {
-    const int r = row0 + 2 * i;
-    if (r >= 2 * Hkv) continue;
-    const bool is_v = r >= Hkv;
-    const int h = is_v ? r - Hkv : r;
-    const long long flat = ((long long)b * Hkv + h) * a.s_max + pos;
-    const long long paged = cell + ((long long)h << a.kv.page_shift);
-    if (TO_PAGES) {
-      in[i] = *reinterpret_cast<const uint4*>((is_v ? a.cv : a.ck) + flat * 128 + d);
-    } else if (FP8) {
-      const uint2 u = *reinterpret_cast<const uint2*>((is_v ? a.kv.v : a.kv.k) + paged * 128 + d);
-      in[i] = make_uint4(u.x, u.y, 0, 0);
-    } else {
-      in[i] = *reinterpret_cast<const uint4*>((is_v ? a.kv.v : a.kv.k) + (paged * 128 + d) * 2);
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      if (i >= n) continue;
+      if (TO_PAGES) {
+        in[z][i] = *reinterpret_cast<const uint4*>(flat_kv[z] + i * flat_step);
+      } else if (FP8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(page_kv[z] + i * page_step);
+        in[z][i] = make_uint4(u.x, u.y, 0, 0);
+      } else {
+        in[z][i] = *reinterpret_cast<const uint4*>(page_kv[z] + i * page_step);
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kRows / 2; ++i) {
-    const int r = row0 + 2 * i;
-    if (r >= 2 * Hkv) continue;
-    const bool is_v = r >= Hkv;
-    const int h = is_v ? r - Hkv : r;
-    const long long flat = ((long long)b * Hkv + h) * a.s_max + pos;
-    const long long paged = cell + ((long long)h << a.kv.page_shift);
-    uint8_t* pool = is_v ? a.kv.v : a.kv.k;
-    uint16_t* cont = is_v ? a.cv : a.ck;
-    if (FP8) {
-      const float scale = (is_v ? a.kv.v_scale : a.kv.k_scale)[h];
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      if (i >= n) continue;
+      uint16_t* fp = flat_kv[z] + i * flat_step;
+      uint8_t* pp = page_kv[z] + i * page_step;
+      if (!FP8) {
+        *reinterpret_cast<uint4*>(TO_PAGES ? pp : reinterpret_cast<uint8_t*>(fp)) = in[z][i];
+        continue;
+      }
+      const float scale = (z ? a.kv.v_scale : a.kv.k_scale)[h0 + 2 * i];
       uint64_t f[4];
       if (TO_PAGES) {
-        unpack8(in[i], f);
-        *reinterpret_cast<uint2*>(pool + paged * 128 + d) = quant8(f, 1.0f / scale);
+        unpack8(in[z][i], f);
+        *reinterpret_cast<uint2*>(pp) = quant8(f, 1.0f / scale);
       } else {
-        const uint32_t w[2] = {in[i].x, in[i].y};
+        const uint64_t s2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
+        const uint32_t w[2] = {in[z][i].x, in[z][i].y};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 p = e4m3x2_to_f32x2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-          f[j] = f2_pack(__float_as_uint(p.x * scale), __float_as_uint(p.y * scale));
+          f[j] = f2_mul(f2_pack(__float_as_uint(p.x), __float_as_uint(p.y)), s2);
         }
-        *reinterpret_cast<uint4*>(cont + flat * 128 + d) = pack8(f);
+        *reinterpret_cast<uint4*>(fp) = pack8(f);
       }
-    } else if (TO_PAGES) {
-      *reinterpret_cast<uint4*>(pool + (paged * 128 + d) * 2) = in[i];
-    } else {
-      *reinterpret_cast<uint4*>(cont + flat * 128 + d) = in[i];
     }
-  }
 }
 
 int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_tokens, const PagedBatch& pb,
@@ -283,7 +285,7 @@ int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_t
   a.cv = cv;
   a.s_max = s_max;
   a.n_tokens = n_tokens;
-  a.n_blocks_tok = (2 * kv.Hkv + kRows - 1) / kRows;
+  a.n_blocks_tok = (kv.Hkv + kHeads - 1) / kHeads;
   a.err = err;
   const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
   if (blocks >= (1ll << 31)) {
