@@ -391,7 +391,7 @@ int qwen3_op_attention_decode_noalloc(const qwen3_config* cfg, const qwen3_bf16*
 /* Per-head QK RMSNorm + rotate-half RoPE + paged KV-cache write of a ragged batch: the paged
  * form of qwen3_op_qk_norm_rope. qkv [n_tokens, (Hq+2Hkv)*D] (row stride ldqkv): q heads are
  * normalised, rotated and written to q_out [n_tokens, Hq*D] (stride ldq; q_out == qkv with
- * ldq == ldqkv runs in place); k heads (normalised, rotated) and v heads are written to
+ * ldq == ldqkv runs in place, other overlaps are not allowed); k heads (normalised, rotated) and v heads are written to
  * their pages. A token whose position is past max_pos or the page table is reported by the
  * device as QWEN3_ECAPACITY, a negative position, a page id outside [0, n_pages) or a
  * decreasing q_start as QWEN3_EINVAL; nothing of that token is written. */
@@ -413,7 +413,10 @@ int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, 
  * tokens past row n_tokens as QWEN3_EINVAL and one past its page table as QWEN3_ECAPACITY, and
  * leaves its rows of o as they were; a page id outside [0, n_pages) is reported as
  * QWEN3_EINVAL, and that sequence's rows of o then hold no meaningful values. Cache rows behind
- * a token's position are never used, whatever they hold (NaN included). */
+ * a sequence's last new token are never used, whatever they hold (NaN included). Those of the
+ * call's own later tokens have weight 0 for the earlier ones; a NaN or infinity in their values
+ * reaches earlier tokens of the same 128-position tile all the same (0 * NaN), as in
+ * qwen3_op_attention_prefill. */
 int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long long ldq, int n_tokens, int max_q,
                              const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, qwen3_bf16* o, long long ldo,
                              void* ws, size_t ws_bytes, void* stream);
@@ -423,7 +426,8 @@ int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long 
  * e4m3 pages, or from pages into a contiguous cache, as bf16. n_tokens >= q_start[B] bounds the
  * positions moved; everything else is left as it was. Moves a prompt that qwen3_block_prefill or
  * qwen3_stack_forward cached into pages, and back for qwen3_block_decode. Errors as
- * qwen3_op_qk_norm_rope_paged (a position past s_max: QWEN3_ECAPACITY). */
+ * qwen3_op_qk_norm_rope_paged (a position past s_max: QWEN3_ECAPACITY); the two caches must not
+ * overlap. */
 int qwen3_op_kv_to_pages(const qwen3_config* cfg, const qwen3_kv_layer* src, int n_tokens,
                          const qwen3_paged_batch* batch, const qwen3_kv_pages* dst, void* stream);
 int qwen3_op_kv_from_pages(const qwen3_config* cfg, const qwen3_kv_pages* src, int n_tokens,

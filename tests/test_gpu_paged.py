@@ -72,8 +72,8 @@ class Case:
     def darken(self):
         seen = np.zeros((self.n_pages, self.page), dtype=bool)
         for b, (t, c) in enumerate(zip(self.qlens, self.ctx)):
-            for p in range(t + c if t else 0):
-                seen[self.table[b, p // self.page], p % self.page] = True
+            p = np.arange(t + c if t else 0)
+            seen[self.table[b, p // self.page], p % self.page] = True
         dark = ~torch.from_numpy(seen).cuda()[:, None, :, None]
         raw, nan = (torch.uint8, 0x7F) if self.fp8 else (torch.int16, 0x7FC0)
         self.k.view(raw).masked_fill_(dark, nan)
@@ -82,8 +82,10 @@ class Case:
     def rows(self, pool, scale, b, n):
         """float64 [n, hkv, D] of a sequence's first n cached positions."""
         p = np.arange(n)
-        raw = f64(pool.float() if self.fp8 else pool)
-        return raw[self.table[b, p // self.page], :, p % self.page] * scale[:, None]
+        page, slot = (torch.from_numpy(x).long().cuda() for x in (self.table[b, p // self.page], p % self.page))
+        raw = pool.view(torch.uint8) if self.fp8 else pool
+        cells = raw[page, :, slot].view(pool.dtype)
+        return f64(cells.float() if self.fp8 else cells) * scale[:, None]
 
     def attend(self, max_q=None, ldo_extra=0, ws=None, stream=None, out=None):
         q3 = self.q3
@@ -295,6 +297,75 @@ def test_attention_reports_bad_sequences(q3, qlens, fp8):
 
     for bad in (-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1):
         run(q3.EINVAL, page(bad), 1, same_rows=False)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_mixed_batch_reports_and_serves(q3, fp8):
+    """A batch large enough for both forms of the kernel, with bad decode and chunk sequences."""
+    qlens = [1, 40, 1, 1, 9, 1, 1, 200, 1, 1, 1, 0, 1, 1, 2, 1, 1, 1]
+    ctx = [50 * i + 3 for i in range(18)]
+    c = Case(q3, qlens, ctx, 32, fp8=fp8, seed=8, pad=2)
+    c.t_ctx[2] = -7
+    c.t_ctx[7] = 10 ** 6
+    o = c.attend()
+    assert q3.check_device_error() in (q3.EINVAL, q3.ECAPACITY)
+    got, (ref, tol) = f64(o), c.reference()
+    for b in range(18):
+        r = slice(c.q_start[b], c.q_start[b + 1])
+        if b in (2, 7):
+            assert (got[r] == 7.0).all()
+        else:
+            assert (np.abs(got[r] - ref[r]) <= tol[r]).all(), b
+    assert (got[c.q_start[-1]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q", [1, 2])
+def test_attention_many_sequences(q3, q, fp8):
+    """More sequences than the plan keeps in shared memory."""
+    B = 1100
+    c = Case(q3, [q if b % 7 else 0 for b in range(B)], [(37 * b) % 200 for b in range(B)], 16, hq=4, hkv=2, fp8=fp8)
+    c.darken()
+    o = c.attend()
+    assert_device_ok()
+    c.check(o)
+
+
+@pytest.mark.parametrize("qlens", [[1, 1], [150, 1]])
+def test_attention_graphs_share_a_workspace(q3, qlens):
+    """Two captured calls with one workspace, replayed in turn on one stream."""
+    cases = [Case(q3, qlens, [4000, 100], 32, seed=1), Case(q3, qlens, [10, 2500], 32, fp8=True, seed=2)]
+    want = [c.attend() for c in cases]
+    n = q3.workspace_size(cases[0].cfg, q3.OP_ATTENTION_PAGED, 2, max(qlens), 1)
+    ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.full_like(w, 7.0) for w in want], []
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.attend(ws=ws, out=o)
+        graphs.append(g)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    assert_device_ok()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o)
+
+
+def test_attention_nan_and_huge_keys_behind_a_token(q3):
+    """Keys of later tokens of the same call may hold anything: their scores are masked."""
+    for fp8 in (False, True):
+        c = Case(q3, [6], [130], 32, fp8=fp8)
+        c.darken()
+        ref, tol = c.reference()
+        p = 135  # the last token's position
+        c.k[int(c.table[0, p // 32]), :, p % 32].view(torch.uint8).fill_(0x7F)
+        o = f64(c.attend())
+        assert_device_ok()
+        assert (np.abs(o[:5] - ref[:5]) <= tol[:5]).all()
+        # the bytes are NaN in e4m3 (and 3.4e38 in bf16, a score like any other)
+        assert not fp8 or np.isnan(o[5]).all()
 
 
 def test_attention_reports_too_many_tokens(q3):
