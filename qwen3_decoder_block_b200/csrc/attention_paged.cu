@@ -2,7 +2,6 @@
 //   o_t = sum_p w_p V_p,  w = softmax_p(q_t K_p / sqrt(128)),  p <= ctx + t,
 // for every query head of a KV group. Two forms: the decode form below (every sequence brings
 // at most one token; the K/V stream bounds it) and the chunk form further down.
-#include <mutex>
 #include "paged.cuh"
 #include "internal.h"
 
@@ -1734,9 +1733,9 @@ Scratch scratch_of(bool chunk, int B, int Hq, int Hkv) {
 // The forms a call runs (bit 0: decode, bit 1: chunk). With more than one new token allowed, the
 // chunk form can take every sequence. A large batch likely decodes most of them, which the
 // decode form streams faster: 30 decode tokens at 100 to 4000 cached beside two chunks of 300 to
-// 512 take 98 us with both forms and 136 us with the chunk form alone (e4m3: 87 and 165). When
-// there are none, both cost two launches more: 8 x 7 tokens at 100 to 4000 cached 44 and 42 us,
-// four tiny prompts 27 and 16 us.
+// 512 take 94 us with both forms and 127 us with the chunk form alone (e4m3: 84 and 152). When
+// there are none, both cost a launch and a wider plan: 8 x 7 tokens at 100 to 4000 cached 41 and
+// 37 us, four tiny prompts 21 and 17 us.
 constexpr int kMixedBatch = 16;
 int forms_of(int B, int max_q) { return max_q == 1 ? 1 : B >= kMixedBatch ? 3 : 2; }
 
