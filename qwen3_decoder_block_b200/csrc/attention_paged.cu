@@ -930,6 +930,12 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 // of it). For P.V a third warpgroup widens V to fp16 in shared memory, which is exact, and P is
 // fp16 scaled to at most 2^15: 2^-11 of each weight, or 2^-31 of the row's largest, is finer
 // than bf16, and one cvt widens two values.
+//
+// bf16 pages: V may hold any bf16, which fp16 cannot, and both operands of a product share
+// their type, so P is rounded to bf16: 2^-9 of each weight, of random sign, against the 2^-9 of
+// the output's own rounding (0.0023 of the output's norm from the exact result, 0.0017 with an
+// exact P). A second term as in the decode form would double the P.V products; the row sum takes
+// P before it is rounded.
 // ============================================================================
 namespace {
 
