@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 // than bf16, and one cvt widens two values.
 //
 // bf16 pages: V may hold any bf16, which fp16 cannot, and both operands of a product share
-// their type, so P is rounded to bf16: 2^-9 of each weight, of random sign, against the 2^-9 of
+// their type, so P is rounded to bf16: at most 2^-8 of each weight, of random sign, beside the 2^-8 of
 // the output's own rounding (0.0023 of the output's norm from the exact result, 0.0017 with an
 // exact P). A second term as in the decode form would double the P.V products; the row sum takes
 // P before it is rounded.
