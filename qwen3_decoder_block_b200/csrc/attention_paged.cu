@@ -1059,6 +1059,22 @@ struct ChunkCfg {
   static constexpr uint32_t kSmem = kOffBar + 40 * 8 + 16 + 1024;
 };
 
+// Byte offset in a Q tile of 16-byte piece c (0 to 15) of a row: two halves of 128 bytes a row,
+// each with the 128-byte swizzle. The next item's q is written by the warps that stage finished
+// rows in the same tile, and no barrier stands between the two: all 16 pieces of a row lie in its own
+// 128 bytes of either half, so that a warp touches the bytes of its 32 rows only, and its own
+// __syncwarp orders them. Staged at 256 bytes a row, a warp's rows would lie on another warp's q.
+__host__ __device__ constexpr uint32_t q_tile_at(int row, int c) {
+  return (uint32_t)(c >> 3) * kTile8 + (uint32_t)row * 128 + (uint32_t)(((c & 7) ^ (row & 7)) << 4);
+}
+constexpr bool q_tile_rows_apart() {
+  for (int row = 0; row < 128; ++row)
+    for (int c = 0; c < 16; ++c)
+      if (q_tile_at(row, c) % kTile8 / 128 != (uint32_t)row || q_tile_at(row, c) / kTile8 != (uint32_t)(c >> 3)) return false;
+  return true;
+}
+static_assert(q_tile_rows_apart(), "a row's pieces stay in its own bytes of the Q tile");
+
 // Tensor memory (512 columns): warpgroup X owns columns [256 X, 256 X + 256): two buffers of 64 for the
 // fp32 scores of half a KV tile, each reused for its 16-bit probabilities, and O_X in the other 128. While
 // the softmax works on one buffer, the tensor core does P.V from the other and the scores that
@@ -1393,9 +1409,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int row = quad * 32 + 2 * i + (lane >> 4);
-          uint8_t* dst = smem + X * C::kQTile + row * 128;
+          uint8_t* dst = smem + X * C::kQTile;
           if (!FP8) {
-            *reinterpret_cast<uint4*>(dst + (d8 >> 3) * kTile8 + (((d8 & 7) ^ (row & 7)) << 4)) = v[i];
+            *reinterpret_cast<uint4*>(dst + q_tile_at(row, d8)) = v[i];
           } else {
             const float dn = __shfl_sync(0xffffffffu, down, (lane & 16) + i);
             const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -1407,7 +1423,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
               t1[j] = pack_e4m3x2(h0, h1);
               t2[j] = pack_e4m3x2(bf16_lo(x[j]) * dn - h0, bf16_hi(x[j]) * dn - h1);
             }
-            uint8_t* d = dst + (((d8 >> 1) ^ (row & 7)) << 4) + (d8 & 1) * 8;
+            uint8_t* d = dst + q_tile_at(row, d8 >> 1) + (d8 & 1) * 8;
             *reinterpret_cast<uint2*>(d) = make_uint2(t1[0] | (t1[1] << 16), t1[2] | (t1[3] << 16));
             *reinterpret_cast<uint2*>(d + kTile8) = make_uint2(t2[0] | (t2[1] << 16), t2[2] | (t2[3] << 16));
           }
@@ -1551,8 +1567,8 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         const float vs = FP8 ? a.kv.v_scale[w.g] : 1.f;
         const float mul = whole ? vs / l_run : 1.f;
         float* part = a.part + ((long long)(blockIdx.x * 2 + (w.k0 > 0 ? 0 : 1)) * 2 + X) * kChunkPart;
-        // finished rows go through the Q tile (whose scores are all done): a row a thread into
-        // shared memory, two whole rows an instruction from there
+        // finished rows go through the Q tile (whose scores are all done), where the warp's own q
+        // lay: a row a thread into shared memory, two whole rows an instruction from there
         uint8_t* stage = smem + X * C::kQTile;
         const bool f16 = a.o_f16 != 0;
 #pragma unroll
@@ -1576,7 +1592,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
               q.y = pack_op_x2(f16, __uint_as_float(o[8 * i + 2]) * mul, __uint_as_float(o[8 * i + 3]) * mul);
               q.z = pack_op_x2(f16, __uint_as_float(o[8 * i + 4]) * mul, __uint_as_float(o[8 * i + 5]) * mul);
               q.w = pack_op_x2(f16, __uint_as_float(o[8 * i + 6]) * mul, __uint_as_float(o[8 * i + 7]) * mul);
-              *reinterpret_cast<uint4*>(stage + r * 256 + (((c * 4 + i) ^ (r & 15)) << 4)) = q;
+              *reinterpret_cast<uint4*>(stage + q_tile_at(r, c * 4 + i)) = q;
             }
           } else if (valid) {
 #pragma unroll
@@ -1595,7 +1611,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
             if (row < n_rows)
               *reinterpret_cast<uint4*>(a.out + (long long)(w.q0 + tile_t0 + (row >> gs)) * a.ldo +
                                         ((long long)(w.g * G + (row & (G - 1))) * kD + 8 * d8)) =
-                  *reinterpret_cast<const uint4*>(stage + row * 256 + ((d8 ^ (row & 15)) << 4));
+                  *reinterpret_cast<const uint4*>(stage + q_tile_at(row, d8));
           }
           __syncwarp();
         }
