@@ -37,7 +37,6 @@ struct PagedAttn {
   KvPages kv;
   int n_tokens, max_q, Hq, g_shift, o_f16;  // g_shift: log2 of the query heads per KV group
   int min_q;         // chunk form: it takes the sequences with at least this many new tokens
-  int beside;        // chunk form: the decode form was launched just before, on its own part of the call
   const uint16_t* q;
   long long ldq;
   uint16_t* out;
@@ -1137,10 +1136,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // After the decode form there is nothing to wait for: it waited for the plan before it let this
-  // kernel start, and the two write different rows. CTAs then start as decode CTAs exit; the
-  // wait at the end keeps this kernel from being complete before that one.
-  if (!a.beside) pdl_wait();
+  pdl_wait();
   pdl_trigger();
   const int Hkv = a.kv.Hkv, n_cta = (int)gridDim.x;
   const CtaStart start = a.start[blockIdx.x];
@@ -1645,7 +1641,6 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (a.beside) pdl_wait();
 }
 
 // Joins the partials of the Q tiles that span CTAs: blocks (c, X, 16 dims) with the tiles that
@@ -1867,7 +1862,6 @@ int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int m
     a.n_cta = num_sms() < cap ? num_sms() : cap;
     ws += off.bytes;
   }
-  form[1].beside = forms == 3 ? 1 : 0;
   form[1].min_q = forms == 3 ? 2 : 1;
   const long long split = forms & 1 && kv.fp8 ? ((long long)pb.B * Hq + kPlanThreads / 32 - 1) / (kPlanThreads / 32) : 0;
   q3_launch(paged_plan_kernel, (unsigned)(2 + split), kPlanThreads, 0, s, form[0], form[1], forms);
