@@ -119,22 +119,28 @@ bool gemm_pair_enabled() {
 
 // The dynamic shared-memory limit of a kernel is a per-device setting: raise it once
 // per (kernel, device), under the lock, and report a failure instead of launching.
-int ensure_smem_attr(const void* func, int bytes, bool* first) {
+int ensure_smem_attr(const void* func, int bytes, int min_regs) {
   const int d = current_device();
   std::lock_guard<std::mutex> lk(g_dev_mu);
-  static std::vector<std::pair<const void*, int>> done;
-  if (first) *first = false;
-  for (const auto& e : done)
-    if (e.first == func && e.second == d) return 0;
-  const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) {
-    set_last_error("cannot raise a kernel's shared memory to %d bytes on device %d: %s", bytes, d,
-                   cudaGetErrorString(e));
-    return -6;
-  }
-  done.emplace_back(func, d);
-  if (first) *first = true;
-  return 0;
+  static ReadyKernels ready;
+  return ready.once(func, d, [&] {
+    if (min_regs > 0) {
+      cudaFuncAttributes fa;
+      const cudaError_t e = cudaFuncGetAttributes(&fa, func);
+      if (e != cudaSuccess || fa.numRegs < min_regs) {
+        set_last_error("a kernel's warpgroup split needs %d registers a thread: %s", min_regs,
+                       e != cudaSuccess ? cudaGetErrorString(e) : "it was built with fewer");
+        return -6;
+      }
+    }
+    const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+      set_last_error("cannot raise a kernel's shared memory to %d bytes on device %d: %s", bytes, d,
+                     cudaGetErrorString(e));
+      return -6;
+    }
+    return 0;
+  });
 }
 
 int* device_error_word() {

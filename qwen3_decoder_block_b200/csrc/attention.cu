@@ -408,17 +408,9 @@ int launch_attention_prefill(const uint16_t* qkv, long long ldqkv, int B, int T,
   p.out = out;
   p.ldo = ldo;
   p.err = err;
-  bool first = false;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(attn_prefill_kernel), kPrefillSmem, &first)) return -6;
-  if (first) {
-    // the register split must fit what the block is launched with, or the increase never returns
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, attn_prefill_kernel) != cudaSuccess ||
-        fa.numRegs * kPrefillThreads < kPrefillRegBudget) {
-      set_last_error("attention prefill: kernel built with too few registers for its warpgroup split");
-      return -6;
-    }
-  }
+  // the register split must fit what the block is launched with, or the increase never returns
+  constexpr int kMinRegs = (kPrefillRegBudget + kPrefillThreads - 1) / kPrefillThreads;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(attn_prefill_kernel), kPrefillSmem, kMinRegs)) return -6;
   const long long n_cta = (long long)p.n_cta_q * Hkv * B;
   if (n_cta >= (1ll << 31)) {
     set_last_error("attention prefill: %lld CTAs exceed the grid limit", n_cta);

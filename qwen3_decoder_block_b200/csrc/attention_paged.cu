@@ -1811,16 +1811,9 @@ int attention_chunk(const PagedAttn& a, cudaStream_t s) {
   CUtensorMap tmK, tmV, tmK16, tmV16;
   if (page_maps(a.kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
   auto kernel = attn_paged_chunk_kernel<FP8>;
-  bool first = false;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem, &first)) return -6;
-  if (first) {
-    // the register split must fit what the block is launched with, or the increase never returns
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs * C::kThreads < C::kRegBudget) {
-      set_last_error("attention_paged: chunk kernel built with too few registers for its warpgroup split");
-      return -6;
-    }
-  }
+  // the register split must fit what the block is launched with, or the increase never returns
+  constexpr int kMinRegs = (C::kRegBudget + C::kThreads - 1) / C::kThreads;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem, kMinRegs)) return -6;
   q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmK, tmV, tmK16, tmV16, a);
   q3_launch(paged_chunk_join_kernel, a.n_cta * 16, 128, 0, s, a);
   return 0;

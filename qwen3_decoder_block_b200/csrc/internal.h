@@ -2,6 +2,8 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <utility>
+#include <vector>
 #include <cuda_runtime.h>
 
 namespace q3 {
@@ -194,10 +196,26 @@ inline cudaError_t q3_launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 b
 
 int* device_error_word();  // device pointer of the library's error word
 
+// What has to succeed once per (kernel, device) before a launch. A failure is returned by every
+// call: only a success is kept. Not thread-safe (the caller holds a lock over the whole step, so
+// that no thread launches while another one is still checking).
+struct ReadyKernels {
+  std::vector<std::pair<const void*, int>> done;
+  template <typename F>
+  int once(const void* func, int device, F&& prepare) {
+    for (const auto& e : done)
+      if (e.first == func && e.second == device) return 0;
+    const int rc = prepare();
+    if (rc == 0) done.emplace_back(func, device);
+    return rc;
+  }
+};
+
 // Raises `func`'s dynamic shared-memory limit to `bytes` on the current device, once per
-// (kernel, device); *first (optional) tells whether this call set it. Returns 0 or -6
-// (with the CUDA error in the last-error message).
-int ensure_smem_attr(const void* func, int bytes, bool* first = nullptr);
+// (kernel, device). min_regs: registers a thread that the kernel must be launched with (a
+// warpgroup split that adds up to more would wait for registers for ever). Returns 0 or -6 (with
+// the reason in the last-error message).
+int ensure_smem_attr(const void* func, int bytes, int min_regs = 0);
 void set_last_error(const char* fmt, ...);
 
 }  // namespace q3
