@@ -1770,53 +1770,42 @@ int page_maps(const KvPages& kv, CUtensorMap* k, CUtensorMap* v, CUtensorMap* k1
   return 0;
 }
 
-template <int G, bool FP8>
-int launch_decode(const PagedAttn& a, const CUtensorMap& tmQ, cudaStream_t s) {
-  using C = DecodeCfg<G, FP8>;
-  CUtensorMap tmK, tmV, tmK16, tmV16;
-  if (page_maps(a.kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
-  auto kernel = attn_paged_decode_kernel<G, FP8>;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem)) return -6;
-  q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmQ, tmK, tmV, tmK16, tmV16, a);
-  return 0;
-}
+// A kernel as it is launched.
+using DecodeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PagedAttn);
+using ChunkKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PagedAttn);
+template <typename K>
+struct Launch {
+  K kernel = nullptr;
+  int threads = 0, smem = 0, min_regs = 0;
+  int ready() const { return ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, min_regs); }
+};
 
-int attention_decode(const PagedAttn& a, cudaStream_t s) {
-  const int G = 1 << a.g_shift, B = a.pb.B;
-  CUtensorMap tmQ;
-  if (a.kv.fp8 ? make_tmap_bytes(&tmQ, a.q8, (long long)B * a.Hq * 2, kD, 2 * G)
-               : make_tmap_3d(&tmQ, a.q, kD, a.Hq, a.n_tokens, kD * 2, a.ldq * 2, 64, G, 1)) {
-    set_last_error("attention_paged: cannot encode the query tensor map");
-    return -6;
+template <int G, bool FP8>
+Launch<DecodeKernel> decode_kernel() {
+  using C = DecodeCfg<G, FP8>;
+  return {attn_paged_decode_kernel<G, FP8>, C::kThreads, (int)C::kSmem, 0};
+}
+Launch<DecodeKernel> decode_kernel(int G, int fp8) {
+  switch (G * 2 + fp8) {
+    case 2: return decode_kernel<1, false>();
+    case 3: return decode_kernel<1, true>();
+    case 4: return decode_kernel<2, false>();
+    case 5: return decode_kernel<2, true>();
+    case 8: return decode_kernel<4, false>();
+    case 9: return decode_kernel<4, true>();
+    case 16: return decode_kernel<8, false>();
+    case 17: return decode_kernel<8, true>();
+    case 32: return decode_kernel<16, false>();
+    case 33: return decode_kernel<16, true>();
   }
-  switch (G * 2 + a.kv.fp8) {
-    case 2: return launch_decode<1, false>(a, tmQ, s);
-    case 3: return launch_decode<1, true>(a, tmQ, s);
-    case 4: return launch_decode<2, false>(a, tmQ, s);
-    case 5: return launch_decode<2, true>(a, tmQ, s);
-    case 8: return launch_decode<4, false>(a, tmQ, s);
-    case 9: return launch_decode<4, true>(a, tmQ, s);
-    case 16: return launch_decode<8, false>(a, tmQ, s);
-    case 17: return launch_decode<8, true>(a, tmQ, s);
-    case 32: return launch_decode<16, false>(a, tmQ, s);
-    case 33: return launch_decode<16, true>(a, tmQ, s);
-  }
-  set_last_error("attention_paged: %d query heads per KV group is not supported (1, 2, 4, 8 or 16)", G);
-  return -2;
+  return {};
 }
 
 template <bool FP8>
-int attention_chunk(const PagedAttn& a, cudaStream_t s) {
+Launch<ChunkKernel> chunk_kernel() {
   using C = ChunkCfg<FP8>;
-  CUtensorMap tmK, tmV, tmK16, tmV16;
-  if (page_maps(a.kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
-  auto kernel = attn_paged_chunk_kernel<FP8>;
   // the register split must fit what the block is launched with, or the increase never returns
-  constexpr int kMinRegs = (C::kRegBudget + C::kThreads - 1) / C::kThreads;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::kSmem, kMinRegs)) return -6;
-  q3_launch(kernel, a.n_cta, C::kThreads, C::kSmem, s, tmK, tmV, tmK16, tmV16, a);
-  q3_launch(paged_chunk_join_kernel, a.n_cta * 16, 128, 0, s, a);
-  return 0;
+  return {attn_paged_chunk_kernel<FP8>, C::kThreads, (int)C::kSmem, (C::kRegBudget + C::kThreads - 1) / C::kThreads};
 }
 
 }  // namespace
@@ -1857,11 +1846,36 @@ int launch_attention_paged(const uint16_t* q, long long ldq, int n_tokens, int m
   }
   form[1].min_q = forms == 3 ? 2 : 1;
   const long long split = forms & 1 && kv.fp8 ? ((long long)pb.B * Hq + kPlanThreads / 32 - 1) / (kPlanThreads / 32) : 0;
+  // all that can fail comes before the first launch: a refused call leaves nothing on the stream
+  CUtensorMap tmQ, tmK, tmV, tmK16, tmV16;
+  if (page_maps(kv, &tmK, &tmV, &tmK16, &tmV16)) return -6;
+  Launch<DecodeKernel> decode;
+  Launch<ChunkKernel> chunk;
+  if (forms & 1) {
+    const int G = 1 << base.g_shift;
+    decode = decode_kernel(G, kv.fp8);
+    if (!decode.kernel) {
+      set_last_error("attention_paged: %d query heads per KV group is not supported (1, 2, 4, 8 or 16)", G);
+      return -2;
+    }
+    if (decode.ready()) return -6;
+    if (kv.fp8 ? make_tmap_bytes(&tmQ, form[0].q8, (long long)pb.B * Hq * 2, kD, 2 * G)
+               : make_tmap_3d(&tmQ, q, kD, Hq, n_tokens, kD * 2, ldq * 2, 64, G, 1)) {
+      set_last_error("attention_paged: cannot encode the query tensor map (ldq %lld)", ldq);
+      return -6;
+    }
+  }
+  if (forms & 2) {
+    chunk = kv.fp8 ? chunk_kernel<true>() : chunk_kernel<false>();
+    if (chunk.ready()) return -6;
+  }
   q3_launch(paged_plan_kernel, (unsigned)(2 + split), kPlanThreads, 0, s, form[0], form[1], forms);
-  int rc = 0;
-  if (forms & 1) rc = attention_decode(form[0], s);
-  if (!rc && forms & 2) rc = kv.fp8 ? attention_chunk<true>(form[1], s) : attention_chunk<false>(form[1], s);
-  if (rc) return rc;
+  if (forms & 1)
+    q3_launch(decode.kernel, form[0].n_cta, decode.threads, decode.smem, s, tmQ, tmK, tmV, tmK16, tmV16, form[0]);
+  if (forms & 2) {
+    q3_launch(chunk.kernel, form[1].n_cta, chunk.threads, chunk.smem, s, tmK, tmV, tmK16, tmV16, form[1]);
+    q3_launch(paged_chunk_join_kernel, form[1].n_cta * 16, 128, 0, s, form[1]);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_last_error("attention_paged launch failed: %s", cudaGetErrorString(e));
