@@ -137,7 +137,7 @@ typedef struct {
   const int* q_start;    /* [B+1] */
   const int* ctx_len;    /* [B] cached positions before this call's tokens */
   const int* page_table; /* [B][max_pages] */
-  int B;
+  int B;                 /* B * Hq below 2^30 */
   int max_pages;         /* max_pages * page_size below 2^31 - 256 */
 } qwen3_paged_batch;
 

@@ -836,7 +836,9 @@ static int check_paged(const qwen3_config& c, const char* what, int n_tokens, co
     if (kv->page_size == 1 << i) shift = i;
   Q3_CHECK(shift > 0, QWEN3_ESHAPE, "%s: page_size (%d) must be 16, 32, 64, 128 or 256", what, kv->page_size);
   Q3_CHECK(kv->n_pages > 0, QWEN3_EINVAL, "%s: n_pages (%d) must be positive", what, kv->n_pages);
-  // cache rows and positions are 32-bit coordinates
+  // cache rows, positions and (sequence, query term) rows are 32-bit coordinates
+  Q3_CHECK((long long)batch->B * c.n_q_heads < (1ll << 30), QWEN3_ESHAPE,
+           "%s: batch->B (%d) * n_q_heads exceeds 2^30", what, batch->B);
   Q3_CHECK((long long)kv->n_pages * c.n_kv_heads * kv->page_size < (1ll << 31) - 256, QWEN3_ESHAPE,
            "%s: n_pages * n_kv_heads * page_size exceeds 2^31 rows", what);
   Q3_CHECK((long long)batch->max_pages * kv->page_size < (1ll << 31) - 256, QWEN3_ESHAPE,
