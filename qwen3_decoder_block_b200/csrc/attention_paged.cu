@@ -23,8 +23,8 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte swizzle: 16 KB
 
 // Where a CTA's share of the work list starts (written by the plan kernel, so that a CTA finds
-// it with one load).
-struct __align__(32) CtaStart {
+// it with one load). Its alignment is the one that a workspace has to have.
+struct __align__(16) CtaStart {
   long long units;  // all units of the call
   int b, g, j;      // sequence, KV group and tile (decode form) or item (chunk form) of its first unit
   int rest;         // decode form: keys of that row; chunk form: units of the item before the CTA's
@@ -1733,6 +1733,7 @@ namespace {
 struct Scratch {
   size_t plan, start, counters, part, q8, q8_scale, bytes;
 };
+static_assert(alignof(CtaStart) <= 16 && alignof(ChunkMeta) <= 16, "a workspace is aligned to 16 bytes");
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 Scratch scratch_of(bool chunk, int B, int Hq, int Hkv) {
   Scratch s;
