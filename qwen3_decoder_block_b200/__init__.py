@@ -44,6 +44,7 @@ class KVLayer(ctypes.Structure):
 
 
 class KVPages(ctypes.Structure):
+    n_kv_heads = None  # of the tensors behind the pointers, where kv_pages saw them
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("fp8", ctypes.c_int)]
@@ -247,7 +248,16 @@ def kv_pages(k, v, k_scale=None, v_scale=None) -> KVPages:
         for t in (k_scale, v_scale):
             if t is None or t.dtype != torch.float32 or t.numel() != k.shape[1] or not t.is_contiguous():
                 raise ValueError("kv_pages: e4m3 pages need contiguous float32 k_scale and v_scale of one value per KV head")
-    return KVPages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[2], 1 if fp8 else 0)
+    pages = KVPages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[2], 1 if fp8 else 0)
+    pages.n_kv_heads = k.shape[1]
+    return pages
+
+
+def _pages_for(cfg, pages: KVPages, where: str):
+    """The pages, whose head count the C struct does not hold, checked against the configuration."""
+    if pages.n_kv_heads is not None and pages.n_kv_heads != cfg.n_kv_heads:
+        raise ValueError(f"{where}: pages of {pages.n_kv_heads} KV heads, but cfg.n_kv_heads is {cfg.n_kv_heads}")
+    return ctypes.byref(pages)
 
 
 def paged_batch(q_start, ctx_len, page_table) -> PagedBatch:
@@ -377,27 +387,28 @@ def op_qk_norm_rope_paged(cfg, qkv, n_tokens, batch, q_norm, k_norm, pages, rope
     if ldq is None:
         ldq = ld if q_out is qkv else width
     _check(lib.qwen3_op_qk_norm_rope_paged(ctypes.byref(cfg), _ptr(qkv), ld, n_tokens, ctypes.byref(batch),
-                                           _ptr(q_norm), _ptr(k_norm), ctypes.byref(pages), _ptr(rope), _ptr(q_out),
-                                           ldq, _stream(stream)), "op_qk_norm_rope_paged")
+                                           _ptr(q_norm), _ptr(k_norm), _pages_for(cfg, pages, "op_qk_norm_rope_paged"),
+                                           _ptr(rope), _ptr(q_out), ldq, _stream(stream)), "op_qk_norm_rope_paged")
 
 
 def op_attention_paged(cfg, q, n_tokens, max_q, batch, pages, o, ws, ldq=None, ldo=None, stream=None) -> None:
     width = cfg.n_q_heads * cfg.head_dim
     _check(lib.qwen3_op_attention_paged(ctypes.byref(cfg), _ptr(q), ldq or width, n_tokens, max_q,
-                                        ctypes.byref(batch), ctypes.byref(pages), _ptr(o), ldo or width, _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream(stream)), "op_attention_paged")
+                                        ctypes.byref(batch), _pages_for(cfg, pages, "op_attention_paged"), _ptr(o),
+                                        ldo or width, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "op_attention_paged")
 
 
 def op_kv_to_pages(cfg, kv, n_tokens, batch, pages, stream=None) -> None:
     """Contiguous cache (kv_layer) -> pages, the batch's positions."""
     _check(lib.qwen3_op_kv_to_pages(ctypes.byref(cfg), ctypes.byref(kv), n_tokens, ctypes.byref(batch),
-                                    ctypes.byref(pages), _stream(stream)), "op_kv_to_pages")
+                                    _pages_for(cfg, pages, "op_kv_to_pages"), _stream(stream)), "op_kv_to_pages")
 
 
 def op_kv_from_pages(cfg, pages, n_tokens, batch, kv, stream=None) -> None:
     """Pages -> contiguous cache (kv_layer), the batch's positions."""
-    _check(lib.qwen3_op_kv_from_pages(ctypes.byref(cfg), ctypes.byref(pages), n_tokens, ctypes.byref(batch),
-                                      ctypes.byref(kv), _stream(stream)), "op_kv_from_pages")
+    _check(lib.qwen3_op_kv_from_pages(ctypes.byref(cfg), _pages_for(cfg, pages, "op_kv_from_pages"), n_tokens,
+                                      ctypes.byref(batch), ctypes.byref(kv), _stream(stream)), "op_kv_from_pages")
 
 
 def op_embed(ids, n, embed, vocab, H, out, stream=None) -> None:
