@@ -131,7 +131,7 @@ typedef struct {
  * ctx_len[b], ctx_len[b] + 1, ...; a sequence may have none. Position p of sequence b lives in
  * page page_table[b * max_pages + p / page_size], slot p % page_size. Entries behind a
  * sequence's last position are not read; sequences may share pages that no call writes.
- * q_start must not decrease; rows q_start[B] .. n_tokens-1 belong to no sequence: they are not
+ * q_start must not decrease, nor leave [0, n_tokens]; rows q_start[B] .. n_tokens-1 belong to no sequence: they are not
  * read as tokens and their outputs are left as they were. */
 typedef struct {
   const int* q_start;    /* [B+1] */
@@ -393,8 +393,9 @@ int qwen3_op_attention_decode_noalloc(const qwen3_config* cfg, const qwen3_bf16*
  * normalised, rotated and written to q_out [n_tokens, Hq*D] (stride ldq; q_out == qkv with
  * ldq == ldqkv runs in place, other overlaps are not allowed); k heads (normalised, rotated) and v heads are written to
  * their pages. A token whose position is past max_pos or the page table is reported by the
- * device as QWEN3_ECAPACITY, a negative position, a page id outside [0, n_pages) or a
- * decreasing q_start as QWEN3_EINVAL; nothing of that token is written. */
+ * device as QWEN3_ECAPACITY, a negative position or a page id outside [0, n_pages) as
+ * QWEN3_EINVAL; nothing of that token is written. A q_start that decreases or leaves
+ * [0, n_tokens] is reported as QWEN3_EINVAL; no token at or behind that entry is written. */
 int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, long long ldqkv, int n_tokens,
                                 const qwen3_paged_batch* batch, const qwen3_bf16* q_norm, const qwen3_bf16* k_norm,
                                 const qwen3_kv_pages* kv, const float* rope, qwen3_bf16* q_out, long long ldq,
@@ -423,8 +424,8 @@ int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long 
 
 /* Copies the batch's positions (ctx_len[b] .. ctx_len[b] + q_start[b+1] - q_start[b] - 1 of sequence b,
  * all KV heads, k and v) from a contiguous cache [B][Hkv][s_max][D] into pages, quantising for
- * e4m3 pages, or from pages into a contiguous cache, as bf16. n_tokens >= q_start[B] bounds the
- * positions moved; everything else is left as it was. Moves a prompt that qwen3_block_prefill or
+ * e4m3 pages, or from pages into a contiguous cache, as bf16. n_tokens: at least q_start[B];
+ * everything else is left as it was. Moves a prompt that qwen3_block_prefill or
  * qwen3_stack_forward cached into pages, and back for qwen3_block_decode. Errors as
  * qwen3_op_qk_norm_rope_paged (a position past s_max: QWEN3_ECAPACITY); the two caches must not
  * overlap. */

@@ -37,6 +37,9 @@ struct NormRopeArgs {
   int* err;
 };
 
+// Blocks of `warps` warps for the items of the tokens and, behind them, the check of the lists.
+long long blocks_of(long long items, int B, int warps) { return (items + ((long long)B + 31) / 32 + warps - 1) / warps; }
+
 // 8 bf16 as four pairs of fp32, and back
 __device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&f)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -71,8 +74,12 @@ __global__ void __launch_bounds__(32 * kNormWarps, 6) qk_norm_rope_paged_kernel(
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+  const long long items = (long long)a.n_tokens * a.n_blocks_tok;
+  if (item >= items) {
+    paged_check_lists(a.pb, a.n_tokens, item - items, lane, a.err);
+    return;
+  }
   const int tok = (int)(item / a.n_blocks_tok);
-  if (tok >= a.n_tokens) return;
   const int Hkv = a.kv.Hkv, slots = a.Hq + 2 * Hkv;
   const int slot0 = (int)(item % a.n_blocks_tok) * kSlotsPerWarp + (lane >> 3);
   const int d = (lane & 7) * 8;
@@ -88,13 +95,13 @@ __global__ void __launch_bounds__(32 * kNormWarps, 6) qk_norm_rope_paged_kernel(
     }
   }
   PagedToken at;
-  if (!paged_seq_of(a.pb, tok, lane, &at)) return;  // a row behind the last sequence
+  if (!paged_seq_of(a.pb, a.n_tokens, tok, lane, &at)) return;
   const int t = tok - at.start;
-  const int pos = at.ctx + t;
-  if (t < 0 || pos >= a.max_pos) {
+  if (t < 0 || at.ctx >= a.max_pos - t) {
     if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
     return;
   }
+  const int pos = at.ctx + t;
   uint64_t cs[4], sn[4];  // of dims d + 2 j, d + 2 j + 1
   {
     // (a negative position is reported below; its row is not read)
@@ -174,7 +181,7 @@ int launch_qk_norm_rope_paged(const uint16_t* qkv, long long ldqkv, int n_tokens
   a.n_blocks_tok = (Hq + 2 * kv.Hkv + kSlotsPerWarp - 1) / kSlotsPerWarp;
   a.eps = eps;
   a.err = err;
-  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kNormWarps - 1) / kNormWarps;
+  const long long blocks = blocks_of((long long)n_tokens * a.n_blocks_tok, pb.B, kNormWarps);
   if (blocks >= (1ll << 31)) {
     set_last_error("qk_norm_rope_paged: %d tokens exceed the grid limit", n_tokens);
     return -2;
@@ -209,17 +216,21 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long items = (long long)a.n_tokens * a.n_blocks_tok;
+  if (item >= items) {
+    paged_check_lists(a.pb, a.n_tokens, item - items, lane, a.err);
+    return;
+  }
   const int tok = (int)(item / a.n_blocks_tok);
-  if (tok >= a.n_tokens) return;
   const int Hkv = a.kv.Hkv;
   PagedToken at;
-  if (!paged_seq_of(a.pb, tok, lane, &at)) return;
+  if (!paged_seq_of(a.pb, a.n_tokens, tok, lane, &at)) return;
   const int t = tok - at.start;
-  const int pos = at.ctx + t;
-  if (t < 0 || pos >= a.s_max) {
+  if (t < 0 || at.ctx >= a.s_max - t) {
     if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
     return;
   }
+  const int pos = at.ctx + t;
   const long long cell = paged_row(a.pb, a.kv, at.b, pos, lane == 0 ? a.err : nullptr);
   if (cell < 0) return;
   constexpr int kIter = kHeads / 2;
@@ -287,7 +298,7 @@ int launch_kv_move(bool to_pages, uint16_t* ck, uint16_t* cv, int s_max, int n_t
   a.n_tokens = n_tokens;
   a.n_blocks_tok = (kv.Hkv + kHeads - 1) / kHeads;
   a.err = err;
-  const long long blocks = ((long long)n_tokens * a.n_blocks_tok + kWarps - 1) / kWarps;
+  const long long blocks = blocks_of((long long)n_tokens * a.n_blocks_tok, pb.B, kWarps);
   if (blocks >= (1ll << 31)) {
     set_last_error("kv move: %d tokens exceed the grid limit", n_tokens);
     return -2;

@@ -25,18 +25,34 @@ struct KvPages {
   int n_pages, page_shift, Hkv, fp8;
 };
 
-// The sequence holding row `tok` (the first that ends behind it; q_start is non-decreasing), with
-// its first row and cached length. Every lane of the warp calls it: 32 sequences a round,
-// one memory latency each. False for a row behind the last sequence.
+// Whether sequence i's rows [first, end) can be rows of a buffer of n_tokens.
+__device__ __forceinline__ bool paged_rows_ok(int first, int end, int n_tokens) {
+  return first >= 0 && end >= first && end <= n_tokens;
+}
+
+// Reports an entry of q_start that decreases or lies outside [0, n_tokens], wherever it is: 32
+// sequences a warp, in warps of their own behind those of the tokens (which leave a token at or
+// behind such an entry alone, below), so that no token's chain of loads grows by the check.
+__device__ __forceinline__ void paged_check_lists(const PagedBatch& pb, int n_tokens, long long warp, int lane, int* err) {
+  const long long i = 32 * warp + lane;
+  if (i < pb.B && !paged_rows_ok(pb.q_start[i], pb.q_start[i + 1], n_tokens)) record_error(err, kErrInvalid);
+}
+
+// The sequence holding row `tok` (the first that ends behind it), with its first row and cached
+// length. Every lane of the warp calls it: 32 sequences a round, one memory latency each. False
+// for a row behind the last sequence, or at or behind a bad entry of q_start.
 struct PagedToken {
   int b, start, ctx;
 };
-__device__ __forceinline__ bool paged_seq_of(const PagedBatch& pb, int tok, int lane, PagedToken* out) {
+__device__ __forceinline__ bool paged_seq_of(const PagedBatch& pb, int n_tokens, int tok, int lane, PagedToken* out) {
   for (int base = 0; base < pb.B; base += 32) {
     const int i = base + lane;
     const bool in = i < pb.B;
     const int end = in ? pb.q_start[i + 1] : 0, first = in ? pb.q_start[i] : 0, ctx = in ? pb.ctx_len[i] : 0;
     const unsigned here = __ballot_sync(0xffffffffu, in && end > tok);
+    const unsigned bad = __ballot_sync(0xffffffffu, in && !paged_rows_ok(first, end, n_tokens));
+    // (up to the sequence found: the lowest bit of `here` and those below it)
+    if (bad & (here ? here ^ (here - 1) : 0xffffffffu)) return false;
     if (here) {
       const int f = __ffs(here) - 1;
       out->b = base + f;

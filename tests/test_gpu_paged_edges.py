@@ -44,3 +44,55 @@ def test_workspace_at_any_16_bytes(q3, qlens, fp8):
         c.check(o)
         assert (whole[:at] == 0xAB).all() and (whole[at + n:] == 0xAB).all()
         whole.fill_(0xAB)
+
+
+def run_writer(q3, what, c, n, s_max=100, seed=0):
+    """One of the writers on random inputs: (tensors it may write, as they were before, row of each token)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    B, width = len(c.ctx), (c.hq + 2 * c.hkv) * D
+    qkv, ck, cv = rnd(n, width), rnd(B, c.hkv, s_max, D), rnd(B, c.hkv, s_max, D)
+    out = torch.full((n, c.hq * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    may = {"norm": [c.k, c.v, out], "to": [c.k, c.v], "from": [ck, cv]}[what]
+    old = [raw(t).clone() for t in may]
+    if what == "norm":
+        q3.op_qk_norm_rope_paged(c.cfg, qkv, n, c.batch, one, one, c.pages, rope_gpu(c.cfg), out)
+    elif what == "to":
+        q3.op_kv_to_pages(c.cfg, q3.kv_layer(ck, cv, s_max), n, c.batch, c.pages)
+    else:
+        q3.op_kv_from_pages(c.cfg, c.pages, n, c.batch, q3.kv_layer(ck, cv, s_max))
+    status = q3.check_device_error()
+    return status, [raw(t) for t in may], old
+
+
+def cells_written(c, what, now, old):
+    """Positions (sequence, position) whose cells changed, from a cache writer's tensors."""
+    changed = (now[0] != old[0]).any(-1).any(1)  # pages: [page, slot]; contiguous: [sequence, position]
+    if what == "from":
+        return {(int(b), int(p)) for b, p in changed.nonzero().tolist()}
+    got = {(int(p), int(s)) for p, s in changed.nonzero().tolist()}
+    where = {(int(c.table[b, p // c.page]), p % c.page): (b, p) for b in range(len(c.ctx)) for p in range(c.table.shape[1] * c.page)
+             if c.table[b, p // c.page] < c.n_pages}
+    return {where[x] for x in got}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["norm", "to", "from"])
+@pytest.mark.parametrize("start,served", [
+    ([3, 0], 0), ([-5, 3], 0), ([0, 10, 5, 20], 10), ([0, 2 ** 31 - 1], 0), ([0, 20, 15], 20), ([0, 5, -1, 20], 5), ([0, 5, 21], 5),
+    ([0] + [4] * 40 + [3] + [20] * 3, 4), ([0] + [20] * 70 + [19], 20)])
+def test_writers_report_bad_row_lists(q3, what, start, served, fp8):
+    """Every decrease, and every entry outside [0, n_tokens], is reported, wherever it stands; the
+    tokens before it are written, none at or behind it."""
+    n, B = 20, len(start) - 1
+    c = Case(q3, [20] * B, [16] * B, 16, fp8=fp8, seed=6)
+    c.t_start.copy_(torch.tensor(start, dtype=torch.int32))
+    status, now, old = run_writer(q3, what, c, n)
+    assert status == q3.EINVAL
+    assert cells_written(c, what, now, old) == {(0, 16 + t) for t in range(served)}
+    if what == "norm":
+        rows = (now[2] != old[2]).any(-1)
+        assert rows[:served].all() and not rows[served:].any()
