@@ -131,8 +131,9 @@ typedef struct {
  * ctx_len[b], ctx_len[b] + 1, ...; a sequence may have none. Position p of sequence b lives in
  * page page_table[b * max_pages + p / page_size], slot p % page_size. Entries behind a
  * sequence's last position are not read; sequences may share pages that no call writes.
- * q_start must not decrease, nor leave [0, n_tokens]; rows q_start[B] .. n_tokens-1 belong to no sequence: they are not
- * read as tokens and their outputs are left as they were. */
+ * q_start must not decrease, nor leave [0, n_tokens]; rows 0 .. q_start[0]-1 and
+ * q_start[B] .. n_tokens-1 belong to no sequence: they are not read as tokens and their outputs
+ * are left as they were. */
 typedef struct {
   const int* q_start;    /* [B+1] */
   const int* ctx_len;    /* [B] cached positions before this call's tokens */

@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(32 * kNormWarps, 6) qk_norm_rope_paged_kernel(
   PagedToken at;
   if (!paged_seq_of(a.pb, a.n_tokens, tok, lane, &at)) return;
   const int t = tok - at.start;
-  if (t < 0 || at.ctx >= a.max_pos - t) {
-    if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
+  if (at.ctx >= a.max_pos - t) {
+    if (lane == 0) record_error(a.err, kErrCapacity);
     return;
   }
   const int pos = at.ctx + t;
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(32 * kWarps) kv_move_kernel(const MoveArgs a) 
   PagedToken at;
   if (!paged_seq_of(a.pb, a.n_tokens, tok, lane, &at)) return;
   const int t = tok - at.start;
-  if (t < 0 || at.ctx >= a.s_max - t) {
-    if (lane == 0) record_error(a.err, t < 0 ? kErrInvalid : kErrCapacity);
+  if (at.ctx >= a.s_max - t) {
+    if (lane == 0) record_error(a.err, kErrCapacity);
     return;
   }
   const int pos = at.ctx + t;

@@ -40,7 +40,8 @@ __device__ __forceinline__ void paged_check_lists(const PagedBatch& pb, int n_to
 
 // The sequence holding row `tok` (the first that ends behind it), with its first row and cached
 // length. Every lane of the warp calls it: 32 sequences a round, one memory latency each. False
-// for a row behind the last sequence, or at or behind a bad entry of q_start.
+// for a row of no sequence (before the first or behind the last), or at or behind a bad entry of
+// q_start.
 struct PagedToken {
   int b, start, ctx;
 };
@@ -58,7 +59,7 @@ __device__ __forceinline__ bool paged_seq_of(const PagedBatch& pb, int n_tokens,
       out->b = base + f;
       out->start = __shfl_sync(0xffffffffu, first, f);
       out->ctx = __shfl_sync(0xffffffffu, ctx, f);
-      return true;
+      return tok >= out->start;
     }
   }
   return false;

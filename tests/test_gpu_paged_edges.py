@@ -96,3 +96,30 @@ def test_writers_report_bad_row_lists(q3, what, start, served, fp8):
     if what == "norm":
         rows = (now[2] != old[2]).any(-1)
         assert rows[:served].all() and not rows[served:].any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["norm", "to", "from", "attend1", "attend7"])
+def test_rows_before_the_first_sequence(q3, what, fp8):
+    """A batch may begin behind row 0 of the token buffers (one of several batches over the same
+    rows): the rows before it belong to no sequence, in all four calls."""
+    one = what == "attend1"
+    qlens, ctx = ([1, 1, 1] if one else [7, 0, 3]), [30, 5, 60]
+    c = Case(q3, qlens, ctx, 16, fp8=fp8, seed=6)
+    first, n = 4, 4 + sum(qlens) + 2
+    c.t_start.add_(first)
+    c.q_start = c.q_start + first
+    c.n = n
+    if what.startswith("attend"):
+        c.q = torch.randn(n, c.hq * D, device="cuda").bfloat16()
+        o = c.attend()
+        assert_device_ok()
+        ref, tol = c.reference()
+        assert (np.abs(f64(o)[first:-2] - ref) <= tol).all() and (o[:first] == 7.0).all() and (o[-2:] == 7.0).all()
+        return
+    status, now, old = run_writer(q3, what, c, n)
+    assert status == q3.OK
+    assert cells_written(c, what, now, old) == {(b, x + t) for b, (m, x) in enumerate(zip(qlens, ctx)) for t in range(m)}
+    if what == "norm":
+        rows = (now[2] != old[2]).any(-1)
+        assert rows[first:-2].all() and not rows[:first].any() and not rows[-2:].any()
