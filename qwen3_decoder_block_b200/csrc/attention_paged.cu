@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
             m_run[jj] = mt;
             rescale = true;
           }
-          p[jj] = (t < nk && m_run[jj] != -INFINITY) ? ex2_approx(s[jj] - m_run[jj]) : 0.f;
+          // (no maximum yet: every score is -inf, of weight 0, or NaN, which stays)
+          p[jj] = t < nk ? ex2_approx(s[jj] - (m_run[jj] == -INFINITY ? 0.f : m_run[jj])) : 0.f;
           l_part[jj] = l_part[jj] * alpha[jj] + p[jj];
         }
         // the set's P buffer and O are free once the P.V of its previous tile is complete

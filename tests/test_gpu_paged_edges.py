@@ -123,3 +123,23 @@ def test_rows_before_the_first_sequence(q3, what, fp8):
     if what == "norm":
         rows = (now[2] != old[2]).any(-1)
         assert rows[first:-2].all() and not rows[:first].any() and not rows[-2:].any()
+
+
+def cells(c, pool, b, first, last):
+    """View-like access to positions first..last-1 of a sequence: index tuple into a page tensor."""
+    p = np.arange(first, last)
+    return (torch.from_numpy(c.table[b, p // c.page]).long().cuda(), slice(None), torch.from_numpy(p % c.page).cuda())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q", [1, 3])
+@pytest.mark.parametrize("ctx,first", [(130, 128), (258, 256), (2, 0), (40000, 39936)])
+def test_nan_keys_of_one_tile_reach_the_output(q3, q, ctx, first, fp8):
+    """A KV tile of which every key is NaN, alone in its partial maximum: the row is NaN, not the mean
+    over the other tiles."""
+    c = Case(q3, [q], [ctx], 128, fp8=fp8, seed=2)
+    c.darken()
+    c.k.view(torch.uint8)[cells(c, c.k, 0, first, ctx + q)] = 0x7F if fp8 else 0xFF
+    o = c.attend()
+    assert_device_ok()
+    assert torch.isnan(o).all()
