@@ -418,7 +418,8 @@ int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, 
  * a sequence's last new token are never used, whatever they hold (NaN included). Those of the
  * call's own later tokens have weight 0 for the earlier ones; a NaN or infinity in their values
  * reaches earlier tokens of the same 128-position tile all the same (0 * NaN), as in
- * qwen3_op_attention_prefill. */
+ * qwen3_op_attention_prefill. An infinity in an attended value gives an infinity (NaN where its
+ * weight is 0 in fp32), as the sum does. */
 int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long long ldq, int n_tokens, int max_q,
                              const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, qwen3_bf16* o, long long ldo,
                              void* ws, size_t ws_bytes, void* stream);

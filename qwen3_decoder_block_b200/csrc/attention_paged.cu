@@ -20,6 +20,7 @@ constexpr int kMaxCtas = 256;              // grid bound
 constexpr int kPartFloats = kD + 2;        // one query row's partial: o[128], running max, sum
 constexpr float kScaleLog2 = 0.12751743074380304f;  // log2(e) / sqrt(128)
 constexpr float kRescaleThreshold = 8.0f;
+constexpr float kTinyWeight = 7.888609e-31f;  // 2^-100
 constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte swizzle: 16 KB
 
 // Where a CTA's share of the work list starts (written by the plan kernel, so that a CTA finds
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
 // two e4m3 terms (exact for bf16 queries) and P as three, each 16 times finer than the last
 // (P scaled so that the running maximum is 2^5 to 2^8 of e4m3's 448: relative error 2^-12, or
 // 2^-23 of the row's largest weight, finer than bf16), in columns [t G, t G + G) of term t. With
-// bf16 pages P enters as two bf16 terms, hi and the rest (2^-16), in the same way.
+// bf16 pages P enters as two bf16 terms, its leading 8 bits and the rest (2^-15), in the same way.
 // Two TMA warps fill rings of K and of V tiles, one box per page; one warp issues S, one P.V; two sets of softmax warps take alternate tiles,
 // a thread owning one key (S) and one head dim (O). A row that spans CTAs leaves partials; the last of them to arrive merges
 // them in CTA order, so the result does not depend on which one that is, and nobody waits.
@@ -733,10 +734,12 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 #pragma unroll
             for (int jj = 0; jj < GH; ++jj) {
               const int row = j0 + jj, low = G + row;
-              const uint16_t hi = to_bf16_bits(p[jj]);
-              *reinterpret_cast<uint16_t*>(pb + row * 128 + ((chunk ^ (row & 7)) << 4)) = hi;
-              *reinterpret_cast<uint16_t*>(pb + low * 128 + ((chunk ^ (low & 7)) << 4)) =
-                  to_bf16_bits(p[jj] - __uint_as_float((uint32_t)hi << 16));
+              // hi is cut, not rounded, and the rest kept above 0 (by 2^-100 of the largest weight), so
+              // that an infinity in V meets weights of one sign only and stays one
+              const uint32_t hi = __float_as_uint(p[jj]) & 0xffff0000u;
+              const float rest = fmaxf(p[jj] - __uint_as_float(hi), kTinyWeight);
+              *reinterpret_cast<uint16_t*>(pb + row * 128 + ((chunk ^ (row & 7)) << 4)) = (uint16_t)(hi >> 16);
+              *reinterpret_cast<uint16_t*>(pb + low * 128 + ((chunk ^ (low & 7)) << 4)) = to_bf16_bits(rest);
             }
           }
           // keys past the last one: zero their V rows (0 * NaN would poison O)

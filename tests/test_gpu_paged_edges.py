@@ -143,3 +143,25 @@ def test_nan_keys_of_one_tile_reach_the_output(q3, q, ctx, first, fp8):
     o = c.attend()
     assert_device_ok()
     assert torch.isnan(o).all()
+
+
+@pytest.mark.parametrize("qlens,ctx", [([1], [200]), ([1, 1], [9000, 40]), ([5], [700]), ([200], [100]), ([1] * 17 + [30], [300] * 18)])
+def test_attended_infinities(q3, qlens, ctx):
+    """bf16 values of +inf and -inf, in dims of their own and in keys whose weights have any bits: the
+    outputs of those dims are the infinities, the others are right."""
+    c = Case(q3, qlens, ctx, 32, seed=5, sharp=0.5)
+    c.darken()
+    ref, tol = c.reference()
+    inf = float("inf")
+    for b, x in enumerate(ctx):
+        for p in (0, 3, x // 2, x - 1):
+            at = cells(c, c.v, b, p, p + 1)
+            v = c.v[at]
+            v[..., 17], v[..., 90] = inf, -inf
+            c.v[at] = v
+    got = f64(c.attend()).reshape(-1, c.hq, D)
+    assert_device_ok()
+    assert (got[..., 17] == inf).all() and (got[..., 90] == -inf).all()
+    keep = np.ones(D, dtype=bool)
+    keep[[17, 90]] = False
+    assert (np.abs(got - ref.reshape(got.shape)) <= tol.reshape(got.shape))[..., keep].all()
