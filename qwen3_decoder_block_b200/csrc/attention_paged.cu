@@ -21,6 +21,7 @@ constexpr int kPartFloats = kD + 2;        // one query row's partial: o[128], r
 constexpr float kScaleLog2 = 0.12751743074380304f;  // log2(e) / sqrt(128)
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kTinyWeight = 7.888609e-31f;  // 2^-100
+constexpr float kMinFactor = 1.1754944e-38f;  // 2^-126
 constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte swizzle: 16 KB
 
 // Where a CTA's share of the work list starts (written by the plan kernel, so that a CTA finds
@@ -1405,6 +1406,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
           down = __uint_as_float((uint32_t)(127 - e) << 23);
           const float up = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23);
           factor = kScaleLog2 * a.kv.k_scale[w.g] * __shfl_sync(0xffffffffu, up, (lane & 1) * 16 + (lane >> 1));
+          // a row of zeros (2^-119) against a small scale: never 0, which times a masked score's -inf is
+          // NaN (the scores, at most 2^24 before it, stay below 2^-100; a NaN stays)
+          if (factor < kMinFactor) factor = kMinFactor;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

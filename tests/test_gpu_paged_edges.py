@@ -165,3 +165,19 @@ def test_attended_infinities(q3, qlens, ctx):
     keep = np.ones(D, dtype=bool)
     keep[[17, 90]] = False
     assert (np.abs(got - ref.reshape(got.shape)) <= tol.reshape(got.shape))[..., keep].all()
+
+
+@pytest.mark.parametrize("ks", [2.0 ** -126, 1e-9, 1.0, 1e18])
+@pytest.mark.parametrize("qlens", [[1, 1], [200, 3], [1] * 17 + [40]])
+def test_zero_and_tiny_queries_under_any_scale(q3, qlens, ks):
+    """Rows of zeros and of the smallest normal values attend evenly, whatever the keys' scale."""
+    c = Case(q3, qlens, [150 + b for b in range(len(qlens))], 16, fp8=True, seed=4)
+    c.darken()
+    c.ks.fill_(ks)
+    c.ks64 = f64(c.ks)
+    c.q.zero_()
+    c.q[1::2, ::3] = 2.0 ** -126
+    c.q[1::2, 1::3] = -(2.0 ** -120)
+    o = c.attend()
+    assert_device_ok()
+    c.check(o)
