@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
   const float mx = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
   // the largest value scaled into [128, 256): 2^-e exact, a power of two in the normal range
   const int ex = (int)((__float_as_uint(mx) >> 23) & 0xff);
-  const int e = min(max(ex - 127 - 7, -119), 119);
+  const int e = min(max(ex - 127 - 7, -119), 120);
   const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
   uint32_t t1 = 0, t2 = 0;
 #pragma unroll
@@ -1402,7 +1402,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
             }
           }
           const int ex = (int)(mx[0] >> 7);
-          const int e = min(max(ex - 127 - 7, -119), 119);
+          const int e = min(max(ex - 127 - 7, -119), 120);
           down = __uint_as_float((uint32_t)(127 - e) << 23);
           const float up = ex == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23);
           factor = kScaleLog2 * a.kv.k_scale[w.g] * __shfl_sync(0xffffffffu, up, (lane & 1) * 16 + (lane >> 1));

@@ -181,3 +181,20 @@ def test_zero_and_tiny_queries_under_any_scale(q3, qlens, ks):
     o = c.attend()
     assert_device_ok()
     c.check(o)
+
+
+@pytest.mark.parametrize("qlens", [[1, 1], [130, 1]])
+def test_queries_at_the_end_of_bf16(q3, qlens):
+    """Queries of 2^127 and above (up to bf16's largest, 3.4e38) over e4m3 keys that bring their
+    scores to a few units: they are scaled into e4m3's range, not past it."""
+    c = Case(q3, qlens, [170, 40], 32, fp8=True, seed=7)
+    sign = torch.where(torch.rand(c.q.shape, device="cuda") < 0.5, -1.0, 1.0)
+    c.q.copy_(sign * (1.75 + 0.24 * torch.rand(c.q.shape, device="cuda")) * 2.0 ** 127)
+    assert torch.isfinite(c.q).all() and float(c.q.abs().max()) > 3.35e38
+    c.ks.fill_(2.0 ** -126)
+    c.ks64 = f64(c.ks)
+    c.k.copy_((torch.randn(c.k.shape, device="cuda") * 0.5).to(c.k.dtype))
+    c.darken()
+    o = c.attend()
+    assert_device_ok()
+    c.check(o)
