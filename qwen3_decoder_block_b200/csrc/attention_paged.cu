@@ -210,8 +210,8 @@ __device__ void write_plan(const PagedAttn& a, long long* wsum, long long* plan_
 // Before the attention: block 0 writes the decode form's work list, block 1 the chunk form's
 // (`forms`: bit 0 and 1). With e4m3 pages the other blocks split each query head of the decode
 // form (one per warp) into two e4m3 terms, q = 2^e (t1 + t2 / 16): t1 keeps 4 significant
-// bits, the remainder of a bf16 value (8 bits) fits the 4 of t2 exactly, down to 2^-14 of
-// the head's largest value, below which the error stays under 2^-22 of that value.
+// bits, the remainder of a bf16 value (8 bits) fits the 4 of t2 exactly, down to 2^-13 of
+// the head's largest value, below which the error is at most 2^-21 of that value.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttn a, const PagedAttn chunk, int forms) {
   pdl_wait();
   pdl_trigger();
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
 // so K and V go from the pages to the tensor core as they are: bf16 pages with kind::f16,
 // e4m3 pages with kind::f8f6f4, never widened in shared memory. What e4m3 operands would
 // cost in precision is bought back in the columns, which are nearly free here: q enters as
-// two e4m3 terms (exact for bf16 queries) and P as three, each 16 times finer than the last
+// two e4m3 terms (exact for bf16 values down to 2^-13 of the head's largest) and P as three, each 16 times finer than the last
 // (P scaled so that the running maximum is 2^5 to 2^8 of e4m3's 448: relative error 2^-12, or
 // 2^-23 of the row's largest weight, finer than bf16), in columns [t G, t G + G) of term t. With
 // bf16 pages P enters as two bf16 terms, its leading 8 bits and the rest (2^-15), in the same way.
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 // by a kernel that follows.
 //
 // e4m3 pages: S takes K as it is (kind::f8f6f4) against q split into two e4m3 terms of one
-// scale (exact for bf16 values down to 2^-10 of the row's largest; below, off by at most 2^-17
+// scale (exact for bf16 values down to 2^-9 of the row's largest; below, off by at most 2^-16
 // of it). For P.V a third warpgroup widens V to fp16 in shared memory, which is exact, and P is
 // fp16 scaled to at most 2^15: 2^-11 of each weight, or 2^-31 of the row's largest, is finer
 // than bf16, and one cvt widens two values.
@@ -1383,8 +1383,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         float down = 1.f;  // e4m3: of row 2 d8 + (lane >> 4), the row that the exchange below leaves here
         if (FP8) {
           // q = 2^e (t1 + t2), the row's largest value scaled into [128, 256): t1 the leading 4
-          // significant bits, t2 the other 4. Largest values by halving exchanges over the 16
-          // lanes of a row: 15 shuffles for 16 rows.
+          // significant bits, t2 the other 4 (a remainder from the rounded t1 would halve the
+          // error of the smallest values, and cost 1 % of a call). Largest values by halving
+          // exchanges over the 16 lanes of a row: 15 shuffles for 16 rows.
           uint32_t mx[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {

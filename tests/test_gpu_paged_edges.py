@@ -198,3 +198,44 @@ def test_queries_at_the_end_of_bf16(q3, qlens):
     o = c.attend()
     assert_device_ok()
     c.check(o)
+
+
+def one_hot_values(c, b, n):
+    """V of position p < 128 is 1 in dim p: output dim p is the weight of position p."""
+    at = cells(c, c.v, b, 0, n)
+    v = torch.zeros(n, c.hkv, D, device="cuda")
+    v[torch.arange(D), :, torch.arange(D)] = 1.0
+    c.v[at] = v.to(c.v.dtype)
+    c.vs.fill_(1.0)
+    c.vs64 = f64(c.vs)
+
+
+@pytest.mark.parametrize("qlen,bound", [(1, 2.0 ** -21), (2, 2.0 ** -16)])
+def test_small_parts_of_a_query_reach_the_scores(q3, qlen, bound):
+    """Weights read back one by one: the score of key p is q_p alone, a value far below the query's
+    largest, which the two e4m3 terms hold to `bound` of that largest (decode and chunk form)."""
+    c = Case(q3, [qlen], [127], 128, fp8=True, seed=1)
+    hq, n = c.hq, 127 + qlen
+    # key p: 448 in dim p (dims 1 to 127), position 0 all zeros
+    k = torch.zeros(n, c.hkv, D, device="cuda")
+    p = torch.arange(1, 127)
+    k[p, :, p] = 448.0
+    c.k.view(torch.uint8).zero_()
+    c.k[cells(c, c.k, 0, 0, n)] = k.to(c.k.dtype)
+    one_hot_values(c, 0, n)
+    # a scale at which an error of the bound moves a score by 0.25
+    ks = 0.25 / (bound * 448 / D ** 0.5)
+    c.ks.fill_(ks)
+    ks = float(c.ks[0])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    size = bound * 2.0 ** (4 * torch.rand(qlen, hq, D, generator=g, device="cuda"))  # scores of 0.25 to 4
+    q = torch.where(torch.rand(qlen, hq, D, generator=g, device="cuda") < 0.5, -size, size)
+    q[..., 0] = 1.0  # the largest value: scaled to 128, the worst case
+    c.q = q.reshape(qlen, -1).bfloat16()
+    w = f64(c.attend()).reshape(qlen, hq, D)[0]
+    assert_device_ok()
+    got = np.log(w[:, 1:127] / w[:, :1])
+    want = f64(c.q).reshape(qlen, hq, D)[0][:, 1:127] * 448 * ks / D ** 0.5
+    # two outputs in bf16 (2^-8 each, in the logarithm 1.01 times that), the probability's terms (2^-11)
+    assert np.abs(got - want).max() <= 0.25 + 2.02 * 2.0 ** -8 + 2.0 ** -10
