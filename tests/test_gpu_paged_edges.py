@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 
 from helpers import assert_device_ok, rope_gpu  # noqa: E402,F401
 from test_gpu_paged import Case, f64  # noqa: E402,F401
+from test_paged_split import HELD, balanced_keys, balanced_scores  # noqa: E402
 
 D = 128
 
@@ -239,3 +240,39 @@ def test_small_parts_of_a_query_reach_the_scores(q3, qlen, bound):
     want = f64(c.q).reshape(qlen, hq, D)[0][:, 1:127] * 448 * ks / D ** 0.5
     # two outputs in bf16 (2^-8 each, in the logarithm 1.01 times that), the probability's terms (2^-11)
     assert np.abs(got - want).max() <= 0.25 + 2.02 * 2.0 ** -8 + 2.0 ** -10
+
+
+@pytest.mark.parametrize("form,qlens,ctx", [("decode e4m3", [1], [2047]), ("decode e4m3", [1, 1], [127, 30000]),
+                                            ("decode bf16", [1], [2047]), ("decode bf16", [1, 1], [127, 30000]),
+                                            ("chunk e4m3", [2], [126]), ("chunk e4m3", [2, 1], [2046, 127])])
+def test_stated_error_of_the_probabilities(q3, form, qlens, ctx):
+    """Values of two groups of keys that nearly cancel: what is left is the error of the weights, which
+    must stay within what the form states (a lost term would not; see test_paged_split.py)."""
+    fp8 = form.endswith("e4m3")
+    c = Case(q3, qlens, ctx, 128, fp8=fp8, gemm_f16=1, seed=2)
+    c.darken()
+    if fp8:
+        c.ks.fill_(D ** 0.5)
+        c.vs.fill_(1.0)
+        c.ks64, c.vs64 = f64(c.ks), f64(c.vs)
+    one = 1.0 if fp8 else D ** 0.5  # a score is the query's value in the dim of the key's kind
+    for b, (t, x) in enumerate(zip(qlens, ctx)):
+        kind = torch.from_numpy(balanced_keys(x + t)).cuda()
+        k = torch.zeros(x + t, c.hkv, D, device="cuda")
+        k.scatter_(2, kind[:, None, None].expand(-1, c.hkv, 1), one)
+        v = torch.tensor([0.0, 1.0, -1.0], device="cuda")[kind][:, None, None].expand(-1, c.hkv, D).clone()
+        v[..., 1::2] *= -1
+        at = cells(c, c.k, b, 0, x + t)
+        c.k[at], c.v[at] = k.to(c.k.dtype), v.to(c.v.dtype)
+    q = torch.zeros(c.n, c.hq, D, device="cuda")
+    q[..., :3] = torch.from_numpy(balanced_scores()).float().cuda()
+    c.q = q.reshape(c.n, -1).bfloat16()
+    got = f64(c.attend())
+    assert_device_ok()
+    ref, loose = c.reference()
+    mag = (loose - 2.0 ** -11 * np.abs(ref) - 1e-7) / (2.0 ** -8 + 2.0 ** -10)
+    # the weights' stated error; e4m3 terms end at 2^-23 of the largest weight (1 in each tile of 128
+    # keys: 2^-16 of it summed over a tile); scores, exponentials and fp32 sums below 2^-16; fp16 output
+    tol = HELD[form][2] * mag + 2.0 ** -16 * mag + (2.0 ** -16 if fp8 else 0) + 2.0 ** -11 * np.abs(ref)
+    assert (np.abs(ref) < 0.03 * mag).all()
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())

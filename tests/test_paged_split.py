@@ -1,4 +1,8 @@
-"""The splits of queries into e4m3 terms, on the host: their stated bounds over every bf16 value."""
+"""The splits of queries and probabilities into terms of fewer bits, on the host: their stated bounds,
+and inputs that would show a lost term of the probabilities."""
+import math
+
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -35,3 +39,63 @@ def test_two_terms_of_a_query(split, exact_from, bound):
     assert bound / 2 * 128 < err.max() <= bound * 128  # the smallest largest value is the worst case
     for largest in (128.0, 255.0):
         assert (err[x >= exact_from * largest] == 0).all()
+
+
+# ---- probabilities. Their rounding errors average out over random weights; so every 128-key tile gets
+# one key M of the largest score (value 0), 41 keys A (value +1) and 86 keys B (value -1), with scores at
+# which the A and the B nearly cancel: the errors of the two weights then are the output.
+HEADS, N_A, N_B = 16, 41, 86
+
+
+def balanced_keys(n):
+    """Kind of each position: 0 M, 1 A, 2 B."""
+    at = np.arange(n) % 128
+    return np.where(at == 0, 0, np.where(at <= N_A, 1, 2))
+
+
+def balanced_scores():
+    """[HEADS, 3] scores of M, A and B before their rounding to bf16."""
+    d = np.linspace(0.31, 2.93, HEADS)
+    return np.stack([0 * d, -d, -d - math.log(N_B / N_A)], 1)
+
+
+def bf16_round(x):
+    return torch.as_tensor(x).float().bfloat16().double()
+
+
+def e4m3_terms(p, terms):
+    """The running maximum lies at 2^5; each term 16 times finer than the one before."""
+    rest, total = p * 32, 0
+    for i in range(terms):
+        t = e4m3(rest * 16 ** i) / 16 ** i
+        total, rest = total + t, rest - t
+    return total / 32
+
+
+def cut_terms(p, terms):
+    """bf16: the leading 8 bits, then the rest."""
+    hi = (p.float().view(torch.int32) & -65536).view(torch.float32).double()
+    return hi if terms == 1 else hi + bf16_round(p - hi)
+
+
+def half_terms(p, terms):
+    """fp16 at 2^7 (bf16 if one bit of detail is lost)."""
+    return (p * 128).half().double() / 128 if terms == 2 else bf16_round(p)
+
+
+# the probabilities of a form: how they are held, terms, stated error of a weight
+HELD = {"decode e4m3": (e4m3_terms, 3, 2.0 ** -12), "decode bf16": (cut_terms, 2, 2.0 ** -15),
+        "chunk e4m3": (half_terms, 2, 2.0 ** -11)}
+
+
+@pytest.mark.parametrize("form", HELD)
+def test_probabilities_and_what_a_lost_term_would_show(form):
+    held, terms, bound = HELD[form]
+    p = torch.exp(bf16_round(balanced_scores()))
+    mag = N_A * p[:, 1] + N_B * p[:, 2]
+    out = lambda w: N_A * w[:, 1] - N_B * w[:, 2]  # noqa: E731
+    tol = bound * mag + 2.0 ** -16 * mag
+    assert (out(p).abs() < 0.02 * mag).all()
+    assert ((out(held(p, terms)) - out(p)).abs() <= tol).all()
+    lost = (out(held(p, terms - 1)) - out(p)).abs()
+    assert (lost > 1.5 * tol).sum() >= 2  # of 16 heads; one is enough to be noticed
