@@ -1759,10 +1759,15 @@ Scratch scratch_of(bool chunk, int B, int Hq, int Hkv) {
 
 // The forms a call runs (bit 0: decode, bit 1: chunk). With more than one new token allowed, the
 // chunk form can take every sequence. A large batch likely decodes most of them, which the
-// decode form streams faster: 30 decode tokens at 100 to 4000 cached beside two chunks of 300 to
-// 512 take 94 us with both forms and 127 us with the chunk form alone (e4m3: 84 and 152). When
-// there are none, both cost a launch and a wider plan: 8 x 7 tokens at 100 to 4000 cached 41 and
-// 37 us, four tiny prompts 21 and 17 us.
+// decode form streams faster. Both forms against the chunk form alone, in us, for two chunks of 300 to
+// 512 tokens in batches of decode tokens at 100 to 4000 cached:
+//   sequences        4          8         12         16         32
+//   bf16       45 / 32    59 / 58    72 / 88    85 / 84   99 / 132
+//   e4m3       50 / 38    59 / 66   69 / 110    82 / 96   91 / 162
+// The lengths, which would tell, are on the device; 16 leaves small batches one form and costs
+// little either way: 15 decode tokens and one chunk 73 / 84 (e4m3 66 / 97). A batch of 16 without a decode
+// token pays the decode form's launch and plan: 16 x 7 tokens 71 / 67 (82 / 79), at 10 to 100
+// cached 20 / 17 (25 / 20).
 constexpr int kMixedBatch = 16;
 int forms_of(int B, int max_q) { return max_q == 1 ? 1 : B >= kMixedBatch ? 3 : 2; }
 
