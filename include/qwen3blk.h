@@ -112,10 +112,10 @@ typedef struct {
 /* One layer's KV cache in pages: k and v are [n_pages][Hkv][page_size][D], with page_size 16,
  * 32, 64, 128 or 256 tokens and n_pages * Hkv * page_size below 2^31 - 256. fp8 = 0: bf16 (the
  * scales are not read). fp8 = 1: e4m3 bytes with one fp32 scale per KV head, k_scale [Hkv]
- * and v_scale [Hkv] (device, positive and finite): a byte stands for its e4m3 value times
- * the head's scale, and a value x is stored as e4m3(x * (1 / scale)), rounded to nearest
- * even, magnitudes above 448 saturated, NaN kept. The attention folds k_scale into the
- * softmax factor and v_scale into the output. */
+ * and v_scale [Hkv] (device; positive, finite and not subnormal, so that 1 / scale is finite): a
+ * byte stands for its e4m3 value times the head's scale, and a value x is stored as
+ * e4m3(x * (1 / scale)), rounded to nearest even, magnitudes above 448 saturated, NaN kept. The
+ * attention folds k_scale into the softmax factor and v_scale into the output. */
 typedef struct {
   void* k;
   void* v;
@@ -408,7 +408,8 @@ int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, 
  * (stride ldo), bf16 (fp16 when cfg->gemm_f16). One call takes any mix of decode tokens
  * (one new token) and prompt chunks.
  *   max_q   upper bound (host) on the new tokens of any sequence; max_q == 1 selects the
- *           decode form of the kernel
+ *           decode form of the kernel; otherwise batches of 16 and more sequences take it for those
+ *           with one new token, and the chunk form for the rest
  *   ws      qwen3_workspace_size(cfg, QWEN3_OP_ATTENTION_PAGED, B, max_q, any) bytes; calls that may
  *           overlap on the GPU need workspaces of their own
  * The device reports a sequence with a negative length or context, more than max_q tokens or
@@ -418,8 +419,11 @@ int qwen3_op_qk_norm_rope_paged(const qwen3_config* cfg, const qwen3_bf16* qkv, 
  * a sequence's last new token are never used, whatever they hold (NaN included). Those of the
  * call's own later tokens have weight 0 for the earlier ones; a NaN or infinity in their values
  * reaches earlier tokens of the same 128-position tile all the same (0 * NaN), as in
- * qwen3_op_attention_prefill. An infinity in an attended value gives an infinity (NaN where its
- * weight is 0 in fp32), as the sum does. */
+ * qwen3_op_attention_prefill. The softmax weights are held to 2^-15 (bf16 pages) or 2^-12 (e4m3) in
+ * the decode form, to 2^-8 or 2^-11 in the chunk form (relative, each; the weights' sum takes them
+ * in fp32): one token's output may differ by that much with the form that its batch selects. An
+ * infinity in an attended value gives an infinity, as the sum does (NaN where its weight is 0 in
+ * fp32). */
 int qwen3_op_attention_paged(const qwen3_config* cfg, const qwen3_bf16* q, long long ldq, int n_tokens, int max_q,
                              const qwen3_paged_batch* batch, const qwen3_kv_pages* kv, qwen3_bf16* o, long long ldo,
                              void* ws, size_t ws_bytes, void* stream);

@@ -939,7 +939,8 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
 // their type, so P is rounded to bf16: at most 2^-8 of each weight, of random sign, beside the 2^-8 of
 // the output's own rounding (0.0023 of the output's norm from the exact result, 0.0017 with an
 // exact P). A second term as in the decode form would double the P.V products; the row sum takes
-// P before it is rounded.
+// P before it is rounded. So a decode token over bf16 pages gets weights of 2^-15 from the decode form
+// and of 2^-8 here, where a chunk in a small batch brings it; the header says so.
 // ============================================================================
 namespace {
 
