@@ -48,9 +48,6 @@ constexpr int kPrefillThreads = 384;  // softmax warpgroups (warps 0-3, 4-7), TM
 constexpr int kPrefillRegsSoftmax = 200;
 constexpr int kPrefillRegsCtl = 88;
 constexpr int kPrefillRegBudget = (2 * kPrefillRegsSoftmax + kPrefillRegsCtl) * 128;
-// log2(e) / sqrt(128)
-constexpr float kScaleLog2 = 0.12751743074380304f;
-constexpr float kRescaleThreshold = 8.0f;
 
 struct PrefillParams {
   int B, T, Hq, Hkv, G, s_max, n_cta_q;
@@ -490,10 +487,6 @@ __device__ __forceinline__ void store_head_dim(float o, int d, uint16_t* dst, co
   dst[d] = hi;
   if (mo.o_lo) dst[mo.o_lo + d] = to_op_bits(mo.o_f16 != 0, o - op_bits_to_f32(mo.o_f16 != 0, hi));
 }
-// CTA c's tile range [c T / n, (c + 1) T / n) is empty (only when T < n).
-__device__ __forceinline__ bool d4_cta_empty(int c, long long T, int n) {
-  return T * c / n == T * (c + 1) / n;
-}
 
 // Merge of one head's partials of a row, by the row's first CTA: its own (m, l, o_d) are
 // in registers and come first in the (deterministic) order; then the CTAs c_first + 1 ..
@@ -504,7 +497,7 @@ __device__ __forceinline__ void merge_row_dim_own(const float* row_base, int c_f
                                                   uint16_t* dst, const DecodeMergeOut& mo) {
   float M = m_own;
   for (int c = c_first + 1; c <= c_last; ++c)
-    if (!d4_cta_empty(c, T, n)) M = fmaxf(M, __ldcg(row_base + c * stride + kHeadDim));
+    if (!cta_empty(c, T, n)) M = fmaxf(M, __ldcg(row_base + c * stride + kHeadDim));
   float L = 0.f, acc = 0.f;
   if (m_own != -INFINITY) {
     const float w = exp2f(m_own - M);
@@ -512,7 +505,7 @@ __device__ __forceinline__ void merge_row_dim_own(const float* row_base, int c_f
     acc = o_own * w;
   }
   for (int c = c_first + 1; c <= c_last; ++c) {
-    if (d4_cta_empty(c, T, n)) continue;
+    if (cta_empty(c, T, n)) continue;
     const float* q = row_base + c * stride;
     const float m = __ldcg(q + kHeadDim);
     if (m == -INFINITY) continue;
@@ -522,37 +515,6 @@ __device__ __forceinline__ void merge_row_dim_own(const float* row_base, int c_f
   }
   store_head_dim(acc / L, d, dst, mo);
 }
-
-// Maximum (MAX) or sum over the 32 lanes of each of G per-lane values, with log2(G) halving
-// exchanges (each leaves a lane the half of the heads its lane bit selects) and then a
-// plain butterfly over the remaining lane bits: G - 1 + 5 - log2(G) shuffles instead of
-// 5 G. Lane l ends with head hd = l >> (5 - log2 G).
-template <int G, bool MAX>
-__device__ __forceinline__ float warp_reduce_heads(const float (&x)[G], int lane) {
-  float a[G];
-#pragma unroll
-  for (int j = 0; j < G; ++j) a[j] = x[j];
-#pragma unroll
-  for (int half = G / 2, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
-    const bool upper = (lane & bit) != 0;
-#pragma unroll
-    for (int k = 0; k < half; ++k) {
-      const float send = upper ? a[k] : a[k + half];
-      const float keep = upper ? a[k + half] : a[k];
-      const float got = __shfl_xor_sync(0xffffffffu, send, bit);
-      a[k] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-#pragma unroll
-  for (int o = 16 / G; o > 0; o >>= 1) {
-    const float got = __shfl_xor_sync(0xffffffffu, a[0], o);
-    a[0] = MAX ? fmaxf(a[0], got) : a[0] + got;
-  }
-  return a[0];
-}
-
-// CTA holding global tile t when T tiles are divided among n CTAs as [c T / n, (c+1) T / n).
-__device__ __forceinline__ int d4_cta_of(long long t, long long T, int n) { return (int)(((t + 1) * n - 1) / T); }
 
 // Walk over the (sequence, group) rows that meet this CTA's tile range. plan[b] is the
 // index of the first tile of sequence b's rows (Hkv rows of plan[b+1]-plan[b] tiles in
@@ -935,7 +897,7 @@ __global__ void __launch_bounds__(d4_threads(G), 1)
         // (where it reaches the row); the others leave a partial in slot row + CTA (unique:
         // the rows and the CTA ranges are both in tile order) and publish it with one
         // release add, without waiting
-        const int c_first = d4_cta_of(w.rs, T, n_cta), c_last = d4_cta_of(w.rs + w.nt - 1, T, n_cta);
+        const int c_first = cta_of(w.rs, T, n_cta), c_last = cta_of(w.rs + w.nt - 1, T, n_cta);
         if ((int)blockIdx.x != c_first) {
           float* my_part = part + ((long long)bg + blockIdx.x) * G * kD4PartFloats;
 #pragma unroll
@@ -956,7 +918,7 @@ __global__ void __launch_bounds__(d4_threads(G), 1)
             // the row's other CTAs (those of (c_first, c_last] whose range is not empty:
             // fewer tiles than CTAs leaves some empty) have all published (bounded wait)
             int n_other = 0;
-            for (int c = c_first + 1; c <= c_last; ++c) n_other += d4_cta_empty(c, T, n_cta) ? 0 : 1;
+            for (int c = c_first + 1; c <= c_last; ++c) n_other += cta_empty(c, T, n_cta) ? 0 : 1;
             bool done = true;
             const unsigned long long t0 = global_ns();
             while (ld_acquire_gpu_s32(&counters[bg]) < n_other) {

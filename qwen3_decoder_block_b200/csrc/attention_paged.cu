@@ -18,8 +18,6 @@ constexpr int kD = 128;
 constexpr int kTileK = 128;                // keys per tile
 constexpr int kMaxCtas = 256;              // grid bound
 constexpr int kPartFloats = kD + 2;        // one query row's partial: o[128], running max, sum
-constexpr float kScaleLog2 = 0.12751743074380304f;  // log2(e) / sqrt(128)
-constexpr float kRescaleThreshold = 8.0f;
 constexpr float kTinyWeight = 7.888609e-31f;  // 2^-100
 constexpr float kMinFactor = 1.1754944e-38f;  // 2^-126
 constexpr uint32_t kTile8 = 128 * 128;     // [128 rows][128 bytes], 128-byte swizzle: 16 KB
@@ -75,11 +73,6 @@ __device__ __forceinline__ bool paged_seq_ok(const PagedAttn& a, int b, int* n_q
   }
   return true;
 }
-
-// CTA holding unit t when U units are divided among n CTAs as [c U / n, (c + 1) U / n).
-__device__ __forceinline__ int cta_of(long long t, long long U, int n) { return (int)(((t + 1) * n - 1) / U); }
-// Whether CTA c's range is empty (only when U < n).
-__device__ __forceinline__ bool cta_empty(int c, long long U, int n) { return U * c / n == U * (c + 1) / n; }
 
 // First unit of CTA c's range.
 __device__ __forceinline__ long long share(long long U, int c, int n) {
@@ -366,33 +359,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
     for (int i = 0; i < 16; ++i) r[16 * c + i] = v[c][i];
 }
 
-// Maximum (MAX) or sum over the 32 lanes of each of G per-lane values: log2(G) halving
-// exchanges, each leaving a lane the half of the heads its lane bit selects, then a butterfly
-// over the other lane bits. Lane l ends with head l >> (5 - log2 G).
-template <int G, bool MAX>
-__device__ __forceinline__ float reduce_heads(const float (&x)[G], int lane) {
-  float a[G];
-#pragma unroll
-  for (int j = 0; j < G; ++j) a[j] = x[j];
-#pragma unroll
-  for (int half = G / 2, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
-    const bool upper = (lane & bit) != 0;
-#pragma unroll
-    for (int k = 0; k < half; ++k) {
-      const float send = upper ? a[k] : a[k + half];
-      const float keep = upper ? a[k + half] : a[k];
-      const float got = __shfl_xor_sync(0xffffffffu, send, bit);
-      a[k] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-#pragma unroll
-  for (int o = 16 / G; o > 0; o >>= 1) {
-    const float got = __shfl_xor_sync(0xffffffffu, a[0], o);
-    a[0] = MAX ? fmaxf(a[0], got) : a[0] + got;
-  }
-  return a[0];
-}
-
 template <int G, bool FP8>
 __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
     attn_paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -674,7 +640,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         // tile maximum per head: the warp's 32 keys, then the 4 quarters
         float* rm = red_max + par * 64;
         {
-          const float wm = reduce_heads<GH, true>(s, lane);
+          const float wm = warp_reduce_heads<GH, true>(s, lane);
           if ((lane & (32 / GH - 1)) == 0) rm[qd * 16 + j0 + lane / (32 / GH)] = wm;
         }
         named_bar(1 + X, 32 * XW);
@@ -775,7 +741,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
         }
       }
       {
-        const float ws = reduce_heads<GH, false>(l_part, lane);
+        const float ws = warp_reduce_heads<GH, false>(l_part, lane);
         if ((lane & (32 / GH - 1)) == 0) red_sum[qd * 16 + j0 + lane / (32 / GH)] = ws;
       }
       named_bar(1 + X, 32 * XW);

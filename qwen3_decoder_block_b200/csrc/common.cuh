@@ -539,4 +539,45 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Maximum (MAX) or sum over the 32 lanes of each of G per-lane values, with log2(G) halving
+// exchanges (each leaves a lane the half of the heads its lane bit selects) and then a
+// plain butterfly over the remaining lane bits: G - 1 + 5 - log2(G) shuffles instead of
+// 5 G. Lane l ends with head hd = l >> (5 - log2 G).
+template <int G, bool MAX>
+__device__ __forceinline__ float warp_reduce_heads(const float (&x)[G], int lane) {
+  float a[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) a[j] = x[j];
+#pragma unroll
+  for (int half = G / 2, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+    const bool upper = (lane & bit) != 0;
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float send = upper ? a[k] : a[k + half];
+      const float keep = upper ? a[k + half] : a[k];
+      const float got = __shfl_xor_sync(0xffffffffu, send, bit);
+      a[k] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+#pragma unroll
+  for (int o = 16 / G; o > 0; o >>= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, a[0], o);
+    a[0] = MAX ? fmaxf(a[0], got) : a[0] + got;
+  }
+  return a[0];
+}
+
+// ----------------------------------------------------------------------------
+// Attention: scores are kept in base 2 (factor log2(e) / sqrt(128)); a running maximum may lag
+// behind by up to 2^kRescaleThreshold before the sums are rescaled.
+// ----------------------------------------------------------------------------
+constexpr float kScaleLog2 = 0.12751743074380304f;
+constexpr float kRescaleThreshold = 8.0f;
+
+// Work divided evenly: CTA c of n takes units [c U / n, (c + 1) U / n) of U.
+// The CTA that holds unit t:
+__device__ __forceinline__ int cta_of(long long t, long long U, int n) { return (int)(((t + 1) * n - 1) / U); }
+// Whether CTA c's range is empty (only when U < n):
+__device__ __forceinline__ bool cta_empty(int c, long long U, int n) { return U * c / n == U * (c + 1) / n; }
+
 }  // namespace q3
