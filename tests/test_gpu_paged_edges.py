@@ -276,3 +276,41 @@ def test_stated_error_of_the_probabilities(q3, form, qlens, ctx):
     tol = HELD[form][2] * mag + 2.0 ** -16 * mag + (2.0 ** -16 if fp8 else 0) + 2.0 ** -11 * np.abs(ref)
     assert (np.abs(ref) < 0.03 * mag).all()
     assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(6, 3), (20, 5), (7, 7), (16, 1)])
+def test_odd_head_counts(q3, hq, hkv, fp8):
+    """All four calls with KV heads that no power of two divides."""
+    for qlens, ctx in (([1, 1, 1], [40, 700, 3]), ([90, 1, 150], [0, 260, 33])):
+        c = Case(q3, qlens, ctx, 16, hq=hq, hkv=hkv, fp8=fp8, seed=hq, pad=1)
+        c.darken()
+        o = c.attend()
+        assert_device_ok()
+        c.check(o)
+        for what in ("norm", "to", "from"):
+            # (pages of their own: read back from pages just filled from it, a cache would not change)
+            c = Case(q3, qlens, ctx, 16, hq=hq, hkv=hkv, fp8=fp8, seed=hq, pad=1)
+            status, now, old = run_writer(q3, what, c, c.n, s_max=800)
+            assert status == q3.OK
+            want = {(b, x + t) for b, (m, x) in enumerate(zip(qlens, ctx)) for t in range(m)}
+            assert cells_written(c, what, now, old) == want
+            # every head of every written cell
+            heads = (now[0] != old[0]).any(-1)
+            heads = heads if what != "from" else heads.transpose(1, 2)
+            per_cell = heads.sum(1 if what != "from" else 2)
+            assert set(per_cell.unique().tolist()) <= {0, hkv}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,max_q", [(1, 1), (5, 1), (3, 40), (20, 40)])
+def test_batches_without_a_token(q3, B, max_q, fp8):
+    """Every sequence empty, rows that belong to none: nothing is written, nothing reported; every
+    form of the attention."""
+    c = Case(q3, [0] * B, [50] * B, 16, fp8=fp8, pad=4, spare=8)
+    o = c.attend(max_q=max_q)
+    assert_device_ok()
+    assert (o == 7.0).all()
+    for what in ("norm", "to", "from"):
+        status, now, old = run_writer(q3, what, c, c.n)
+        assert status == q3.OK and all(torch.equal(a, b) for a, b in zip(now, old))
