@@ -778,13 +778,14 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       }
       named_bar(3, 32 * SW);
       if (X == 1) continue;
+      // (applied last: before the division by the sum it may overflow, folded into 1 / sum be subnormal)
       const float vs = FP8 ? a.kv.v_scale[g] : 1.f;
       uint16_t* out_row = a.out + a.pb.q_start[b] * a.ldo + (long long)g * G * kD + t;
       if (jb == 0 && je == w.nt) {
         if (ok) {
 #pragma unroll
           for (int jj = 0; jj < GH; ++jj)
-            out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, o[jj] * vs / l[jj]);
+            out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, o[jj] / l[jj] * vs);
         }
         continue;
       }
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(DecodeCfg<G, FP8>::kThreads, 1)
       }
 #pragma unroll
       for (int jj = 0; jj < GH; ++jj)
-        out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, acc[jj] * vs / warp_sum(L[jj]));
+        out_row[(j0 + jj) * kD] = to_op_bits(a.o_f16 != 0, acc[jj] / warp_sum(L[jj]) * vs);
     }
     if (!ok) *s_abort = 1;
   }
@@ -1537,7 +1538,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
         tc_fence_after();
         const bool whole = w.k0 == 0 && w.k1 >= nk;
         const float vs = FP8 ? a.kv.v_scale[w.g] : 1.f;
-        const float mul = whole ? vs / l_run : 1.f;
+        const float inv = whole ? 1.f / l_run : 1.f;
+        // one value of a finished row; the scale last, as in the decode form
+        auto done = [&](uint32_t x) { return FP8 ? __uint_as_float(x) * inv * vs : __uint_as_float(x) * inv; };
         float* part = a.part + ((long long)(blockIdx.x * 2 + (w.k0 > 0 ? 0 : 1)) * 2 + X) * kChunkPart;
         // finished rows go through the Q tile (whose scores are all done), where the warp's own q
         // lay: a row a thread into shared memory, two whole rows an instruction from there
@@ -1560,10 +1563,10 @@ __global__ void __launch_bounds__(ChunkCfg<FP8>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 q;
-              q.x = pack_op_x2(f16, __uint_as_float(o[8 * i + 0]) * mul, __uint_as_float(o[8 * i + 1]) * mul);
-              q.y = pack_op_x2(f16, __uint_as_float(o[8 * i + 2]) * mul, __uint_as_float(o[8 * i + 3]) * mul);
-              q.z = pack_op_x2(f16, __uint_as_float(o[8 * i + 4]) * mul, __uint_as_float(o[8 * i + 5]) * mul);
-              q.w = pack_op_x2(f16, __uint_as_float(o[8 * i + 6]) * mul, __uint_as_float(o[8 * i + 7]) * mul);
+              q.x = pack_op_x2(f16, done(o[8 * i + 0]), done(o[8 * i + 1]));
+              q.y = pack_op_x2(f16, done(o[8 * i + 2]), done(o[8 * i + 3]));
+              q.z = pack_op_x2(f16, done(o[8 * i + 4]), done(o[8 * i + 5]));
+              q.w = pack_op_x2(f16, done(o[8 * i + 6]), done(o[8 * i + 7]));
               *reinterpret_cast<uint4*>(stage + q_tile_at(r, c * 4 + i)) = q;
             }
           } else if (valid) {
@@ -1685,16 +1688,18 @@ __global__ void __launch_bounds__(128) paged_chunk_join_kernel(const PagedAttn a
   }
   if (!valid) return;
   const int gs = a.g_shift, G = 1 << gs;
-  const float mul = (a.kv.fp8 ? a.kv.v_scale[m.g] : 1.f) / L;
+  const float inv = 1.f / L, vs = a.kv.fp8 ? a.kv.v_scale[m.g] : 1.f;  // (the scale last, as above)
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = o[j] * inv * vs;
   uint16_t* dst = a.out + (long long)(m.tok + (r >> gs)) * a.ldo + (long long)(m.g * G + (r & (G - 1))) * kD + d0;
   const bool f16 = a.o_f16 != 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4 q;
-    q.x = pack_op_x2(f16, o[8 * h] * mul, o[8 * h + 1] * mul);
-    q.y = pack_op_x2(f16, o[8 * h + 2] * mul, o[8 * h + 3] * mul);
-    q.z = pack_op_x2(f16, o[8 * h + 4] * mul, o[8 * h + 5] * mul);
-    q.w = pack_op_x2(f16, o[8 * h + 6] * mul, o[8 * h + 7] * mul);
+    q.x = pack_op_x2(f16, o[8 * h], o[8 * h + 1]);
+    q.y = pack_op_x2(f16, o[8 * h + 2], o[8 * h + 3]);
+    q.z = pack_op_x2(f16, o[8 * h + 4], o[8 * h + 5]);
+    q.w = pack_op_x2(f16, o[8 * h + 6], o[8 * h + 7]);
     *reinterpret_cast<uint4*>(dst + 8 * h) = q;
   }
 }

@@ -314,3 +314,18 @@ def test_batches_without_a_token(q3, B, max_q, fp8):
     for what in ("norm", "to", "from"):
         status, now, old = run_writer(q3, what, c, c.n)
         assert status == q3.OK and all(torch.equal(a, b) for a, b in zip(now, old))
+
+
+@pytest.mark.parametrize("vs", [2.0 ** -126, 1e-30, 1e35])
+@pytest.mark.parametrize("qlens,ctx", [([1, 1], [30000, 700]), ([1], [60]), ([300, 1], [0, 40]), ([40], [9000]), ([1] * 17 + [40], [300] * 18)])
+def test_values_of_any_scale(q3, qlens, ctx, vs):
+    """The values' scale from the smallest normal number to one that brings 448 near fp32's end: whole
+    rows and rows joined from partials."""
+    c = Case(q3, qlens, ctx, 32, fp8=True, seed=9)
+    c.darken()
+    c.vs.fill_(vs)
+    c.vs64 = np.ones(c.hkv)  # the reference in units of the scale
+    ref, tol = c.reference()
+    got = f64(c.attend()) / float(c.vs[0])
+    assert_device_ok()
+    assert (np.abs(got - ref) <= tol + 2.0 ** -134 / vs).all()  # bf16 ends at steps of 2^-133
