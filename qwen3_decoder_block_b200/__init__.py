@@ -235,7 +235,8 @@ def kv_layer(k, v, s_max: int) -> KVLayer:
 
 def kv_pages(k, v, k_scale=None, v_scale=None) -> KVPages:
     """Pages of one layer's cache: k and v [n_pages, Hkv, page_size, 128], bf16, or
-    float8_e4m3fn with fp32 scales [Hkv]. The struct holds raw pointers: keep the tensors."""
+    float8_e4m3fn with fp32 scales [Hkv]. The struct holds raw pointers: keep the tensors. Calls with a
+    configuration of another KV head count refuse the pages."""
     import torch
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[3] != 128:
         raise ValueError("kv_pages: k and v must share their type and shape [n_pages, Hkv, page_size, 128]")
